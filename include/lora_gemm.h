@@ -325,6 +325,186 @@ size_t lg_mx_scale_bytes(int64_t rows, int K);
 lg_status lg_mx_quantize(const void* in, int64_t rows, int K, void* codes, void* scales, void* stream);
 
 /* ------------------------------------------------------------------------
+ * lg_mxfp4_quantize -- MXFP4 quantization of bf16 rows along K: the 4-bit
+ * format of the OCP Microscaling (MX) family lg_mx_quantize belongs to.
+ *
+ *   blocks of 32 consecutive values along K share the scale 2^e with
+ *   e = floor(log2 max|v|) - 2 clamped to [-127, 127] (-127 for an all-zero
+ *   block), stored as the E8M0 byte e + 127; each value becomes the E2M1 code
+ *   of v 2^-e (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), round to
+ *   nearest even, saturated at +-6.  A block that holds a NaN or an infinity
+ *   gets the scale byte 255 (the E8M0 NaN) and codes 0: E2M1 has neither.
+ *
+ *   in      DEVICE [rows, K] bf16 row-major.
+ *   codes   DEVICE [rows, K / 2] uint8 row-major: value k of a row in byte
+ *           k / 2, even k in the low four bits.
+ *   scales  DEVICE lg_mx_scale_bytes(rows, K) bytes, the blocked layout of
+ *           lg_mx_quantize (rows past `rows`, up to the next multiple of 128,
+ *           get byte 0).
+ *
+ * lg_mxfp4_dequantize is the way back: out [rows, K] bf16 = code value x 2^e,
+ * exact (NaN for a block whose scale byte is 255; a product past bf16's range,
+ * which no scale of lg_mxfp4_quantize gives, becomes an infinity).
+ *
+ * Shapes: 0 <= rows < 2^31; K a multiple of 128.  All pointers 16-byte
+ * aligned; no output may overlap another buffer.
+ * ---------------------------------------------------------------------- */
+lg_status lg_mxfp4_quantize(const void* in, int64_t rows, int K, void* codes, void* scales, void* stream);
+lg_status lg_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int K, void* out,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * lg_lora_linear_mxfp4 -- lg_lora_linear with the base term as MXFP4 products
+ * on the 4-bit block-scaled tensor cores:
+ *
+ *   y[M, N] = deq(x_codes) deq(W_codes)^T + (x A_cat^T) B_cat^T
+ *
+ * The LoRA term comes from the bf16 x, in bf16 with FP32 accumulation, as in
+ * lg_lora_linear_mxfp8 (x may be null when R == 0).
+ *
+ *   x_codes [M, K / 2], x_scales   lg_mxfp4_quantize(x) (or the codes that
+ *                                  lg_block_norm wrote beside x).
+ *   W_codes [N, K / 2], W_scales   lg_mxfp4_quantize(W).
+ *   workspace  lg_lora_linear_mxfp4_workspace_size(M, K, N, R) bytes, 16-byte
+ *              aligned.  Calls that can overlap on the GPU need one each.
+ *
+ * Shapes: 0 <= M < 2^31; K a multiple of 128; N a multiple of 32; R a
+ * multiple of 64, 0 <= R <= 576.  A block scale of 255 makes the outputs that
+ * its row or column reaches NaN.
+ * ---------------------------------------------------------------------- */
+size_t lg_lora_linear_mxfp4_workspace_size(int64_t M, int K, int N, int R);
+lg_status lg_lora_linear_mxfp4(const void* x, const void* x_codes, const void* x_scales,
+                               const void* W_codes, const void* W_scales, const float* A_cat,
+                               const float* B_cat, void* y, int64_t M, int K, int N, int R,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * lg_block_norm -- what lies between two blocks of the transformer: the norm
+ * after one, its gate and the scaled residual, and the modulated norm before
+ * the next, in one pass over the rows:
+ *
+ *   h'[m] = alpha h[m] + gate[s] * N_post(b[m])          s = m / segment_tokens
+ *   n[m]  = N_pre(h'[m]) * (1 + scale[s]) + shift[s]
+ *
+ *   N(v) = v / sqrt(mean(v^2) + eps)                     LG_NORM_RMS
+ *   N(v) = (v - mean v) / sqrt(mean((v - mean v)^2) + eps)   LG_NORM_LAYER
+ *   N(v) = v                                             LG_NORM_NONE
+ *
+ * Statistics and sums are FP32.  h' is rounded to the stream's type when it
+ * is stored, and N_pre reads the stored value, so that a backward pass that
+ * keeps only h' sees what this call saw.  n is rounded to bf16; its codes are
+ * those of the rounded n, bit for bit what lg_mxfp4_quantize(n) or
+ * lg_mx_quantize(n) writes.
+ *
+ * A learned norm weight w is a gate or a (scale = w - 1) of one segment.
+ *
+ *   h, h_out  DEVICE [M, D] residual stream, bf16 or FP32 (stream_type).
+ *             h_out == h (in place) is allowed.
+ *   b         DEVICE [M, D] bf16, the block's output; null for the norm that
+ *             opens a network: then h' = h, and h_out and gate are null,
+ *             post LG_NORM_NONE and alpha 1.
+ *   gate, scale, shift   DEVICE [S, D] FP32, S = ceil(M / segment_tokens);
+ *             null reads as 1, 0, 0.
+ *   n         DEVICE [M, D] bf16, or null when only codes are wanted.
+ *   codes, scales   written when codes_format is LG_CODES_MXFP8 ([M, D] E4M3)
+ *             or LG_CODES_MXFP4 ([M, D / 2] E2M1): scales hold
+ *             lg_mx_scale_bytes(M, D) bytes.  Null for LG_CODES_NONE.
+ *   pre == LG_NORM_NONE: only h' is wanted (the stream's last addition); n,
+ *             scale and shift are null and codes_format is LG_CODES_NONE.
+ *
+ * Shapes: 0 <= M < 2^31, D a multiple of 8 (of 128 with codes), 8 <= D <=
+ * 16384, segment_tokens >= 1; eps > 0 and finite, alpha finite.  All pointers
+ * 16-byte aligned; apart from h_out == h no output may overlap another buffer.
+ * ---------------------------------------------------------------------- */
+#define LG_NORM_NONE 0
+#define LG_NORM_RMS 1
+#define LG_NORM_LAYER 2
+#define LG_STREAM_BF16 0
+#define LG_STREAM_FP32 1
+#define LG_CODES_NONE 0
+#define LG_CODES_MXFP8 1
+#define LG_CODES_MXFP4 2
+
+typedef struct lg_block_norm_args {
+  const void* h;
+  const void* b;
+  const float* gate;
+  const float* scale;
+  const float* shift;
+  void* h_out;
+  void* n;
+  void* codes;
+  void* scales;
+  int64_t M;
+  int64_t segment_tokens;
+  int D;
+  int stream_type;
+  int post;
+  int pre;
+  int codes_format;
+  float alpha;
+  float eps;
+} lg_block_norm_args;
+
+lg_status lg_block_norm(const lg_block_norm_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * lg_block_norm_backward -- the gradients of lg_block_norm.  With dn and
+ * dh_out the gradients that reach n and h_out, x^ = N_pre(h'), u = N_post(b)
+ * and J^T the transposed derivative of a norm at its input:
+ *
+ *   dh' = dh_out + J_pre^T (dn * (1 + scale))
+ *   dh  = alpha dh'            db = J_post^T (gate * dh')
+ *   dgate[s]  = sum over the segment's rows of dh' * u
+ *   dscale[s] = sum of dn * x^           dshift[s] = sum of dn
+ *
+ * The norms' statistics are taken again from h_out and b: nothing but the
+ * forward call's h_out and its inputs is kept.  Sums are FP32, in an order
+ * that the sizes alone set: equal inputs give equal bits.
+ *
+ *   dn        DEVICE [M, D] bf16; null exactly when pre is LG_NORM_NONE.
+ *   dh_out    DEVICE [M, D] of the stream's type, or null for zero (only
+ *             with dn).
+ *   h_out     DEVICE [M, D], as lg_block_norm wrote it (its h where b is
+ *             null).  b, gate, scale as in the forward call.
+ *   dh        DEVICE [M, D] of the stream's type; dh == dh_out is allowed.
+ *   db        DEVICE [M, D] bf16; with b only.
+ *   dgate     DEVICE [S, D] FP32; with b only.  dscale, dshift: with dn only.
+ *   Any of the five outputs may be null, not all of them.
+ *   workspace lg_block_norm_backward_workspace_size(M, D, segment_tokens)
+ *             bytes, 16-byte aligned.  Calls that can overlap on the GPU need
+ *             one each.
+ *
+ * Shapes as for lg_block_norm.  Apart from dh == dh_out no output may overlap
+ * another buffer.
+ * ---------------------------------------------------------------------- */
+typedef struct lg_block_norm_backward_args {
+  const void* dn;
+  const void* dh_out;
+  const void* h_out;
+  const void* b;
+  const float* gate;
+  const float* scale;
+  void* dh;
+  void* db;
+  float* dgate;
+  float* dscale;
+  float* dshift;
+  int64_t M;
+  int64_t segment_tokens;
+  int D;
+  int stream_type;
+  int post;
+  int pre;
+  float alpha;
+  float eps;
+} lg_block_norm_backward_args;
+
+size_t lg_block_norm_backward_workspace_size(int64_t M, int D, int64_t segment_tokens);
+lg_status lg_block_norm_backward(const lg_block_norm_backward_args* args, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * lg_renoise -- partial re-noise of an upscaled latent:
  *
  *   x[i] = (1 - sigma) * up[i] + sigma * eps[offset + i],  i in [0, n)

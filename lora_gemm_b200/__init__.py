@@ -30,8 +30,34 @@ LG_ERR_NOT_SM100 = 7
 # LG_NOALLOC_SCRATCH_BYTES).
 LG_NOALLOC_SCRATCH_BYTES = 48 << 20
 
+# Norm kinds, stream types and code formats of the block norms (the header's LG_NORM_*, LG_STREAM_*, LG_CODES_*).
+_NORM = {None: 0, "rms": 1, "layer": 2}
+_STREAM = {torch.bfloat16: 0, torch.float32: 1}
+_CODES = {None: 0, "mxfp8": 1, "mxfp4": 2}
+
 # Exported C symbols and their ctypes signatures (the header's declarations).
 _c_void_p = ctypes.c_void_p
+
+
+class BlockNormArgs(ctypes.Structure):
+    """lg_block_norm_args."""
+
+    _fields_ = [(f, _c_void_p) for f in ("h", "b", "gate", "scale", "shift", "h_out", "n", "codes", "scales")] + [
+        ("M", ctypes.c_int64), ("segment_tokens", ctypes.c_int64), ("D", ctypes.c_int),
+        ("stream_type", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int), ("codes_format", ctypes.c_int),
+        ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class BlockNormBackwardArgs(ctypes.Structure):
+    """lg_block_norm_backward_args."""
+
+    _fields_ = [(f, _c_void_p) for f in ("dn", "dh_out", "h_out", "b", "gate", "scale", "dh", "db", "dgate", "dscale",
+                                         "dshift")] + [
+        ("M", ctypes.c_int64), ("segment_tokens", ctypes.c_int64), ("D", ctypes.c_int),
+        ("stream_type", ctypes.c_int), ("post", ctypes.c_int), ("pre", ctypes.c_int), ("alpha", ctypes.c_float),
+        ("eps", ctypes.c_float)]
+
+
 _SIGNATURES = {
     "lg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "lg_version": (ctypes.c_int, []),
@@ -77,6 +103,21 @@ _SIGNATURES = {
     ),
     "lg_mx_scale_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int]),
     "lg_mx_quantize": (ctypes.c_int, [_c_void_p, ctypes.c_int64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p]),
+    "lg_mxfp4_quantize": (ctypes.c_int, [_c_void_p, ctypes.c_int64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p]),
+    "lg_mxfp4_dequantize": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int64, ctypes.c_int, _c_void_p, _c_void_p]),
+    "lg_lora_linear_mxfp4_workspace_size": (
+        ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    ),
+    "lg_lora_linear_mxfp4": (
+        ctypes.c_int,
+        [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, ctypes.c_int64,
+         ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p],
+    ),
+    "lg_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), _c_void_p]),
+    "lg_block_norm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]),
+    "lg_block_norm_backward": (
+        ctypes.c_int, [ctypes.POINTER(BlockNormBackwardArgs), _c_void_p, ctypes.c_size_t, _c_void_p]
+    ),
     "lg_renoise": (
         ctypes.c_int,
         [_c_void_p, _c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _c_void_p],
@@ -160,6 +201,14 @@ def _same_device(ref, *tensors):
     for t in tensors:
         if t is not None and t.device != ref.device:
             raise ValueError(f"all tensors must be on {ref.device}, got one on {t.device}")
+
+
+def _launch(device, fn, *args):
+    """fn(*args, current stream of device), with device current."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device))
 
 
 def _scales(pair, rows, K, what):
@@ -449,6 +498,234 @@ def lora_linear_noalloc(x, W, A_cat, B_cat, y):
                                         _stream(x.device))
     _check(st, "lg_lora_linear_noalloc")
     return y
+
+
+def mxfp4_quantize(x, codes=None, scales=None):
+    """MXFP4 of bf16 rows x [rows, K] along K: (E2M1 codes uint8 [rows, K / 2],
+    two per byte, E8M0 scales uint8 in mx_quantize's blocked layout)."""
+    _need(x, torch.bfloat16, "x", 2)
+    rows, K = x.shape
+    nscales = mx_scale_bytes(rows, K)
+    if codes is None:
+        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    else:
+        _need(codes, torch.uint8, "codes", 2)
+        _shape(codes, (rows, K // 2), "codes")
+    if scales is None:
+        scales = torch.empty(nscales, dtype=torch.uint8, device=x.device)
+    else:
+        _at_least(scales, nscales, "scales")
+    _same_device(x, codes, scales)
+    _check(_launch(x.device, lib.lg_mxfp4_quantize, _ptr(x), rows, K, _ptr(codes), _ptr(scales)), "lg_mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None):
+    """The bf16 values [rows, K] that MXFP4 codes [rows, K / 2] and scales stand for (exact)."""
+    _need(codes, torch.uint8, "codes", 2)
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    _at_least(scales, mx_scale_bytes(rows, K), "scales")
+    if out is None:
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
+    else:
+        _need(out, torch.bfloat16, "out", 2)
+        _shape(out, (rows, K), "out")
+    _same_device(codes, scales, out)
+    _check(_launch(codes.device, lib.lg_mxfp4_dequantize, _ptr(codes), _ptr(scales), rows, K, _ptr(out)),
+           "lg_mxfp4_dequantize")
+    return out
+
+
+def lora_linear_mxfp4_workspace_size(M, K, N, R):
+    return int(lib.lg_lora_linear_mxfp4_workspace_size(int(M), int(K), int(N), int(R)))
+
+
+def lora_linear_mxfp4(x, x_mx, W_mx, A_cat, B_cat, y=None, workspace=None):
+    """lora_linear with the base term as MXFP4 products: x_mx = mxfp4_quantize(x)
+    (or the codes block_norm wrote with it), W_mx = mxfp4_quantize(W) (pairs of
+    codes and scales); the LoRA term from the bf16 x, which may be None without
+    adapters.  K must be a multiple of 128."""
+    xq, xsf = x_mx
+    wq, wsf = W_mx
+    _need(xq, torch.uint8, "x codes", 2)
+    _need(wq, torch.uint8, "W codes", 2)
+    M, K, N = xq.shape[0], 2 * xq.shape[1], wq.shape[0]
+    if wq.shape[1] != xq.shape[1]:
+        raise ValueError(f"W codes must have shape {(N, K // 2)}, got {tuple(wq.shape)}")
+    _at_least(xsf, mx_scale_bytes(M, K), "x scales")
+    _at_least(wsf, mx_scale_bytes(N, K), "W scales")
+    R = 0
+    if A_cat is not None and A_cat.numel() > 0:
+        _need(A_cat, torch.float32, "A_cat", 2)
+        _need(B_cat, torch.float32, "B_cat", 2)
+        R = A_cat.shape[0]
+        if A_cat.shape[1] != K or tuple(B_cat.shape) != (N, R):
+            raise ValueError("A_cat must be [R, K] and B_cat [N, R]")
+    else:
+        A_cat = B_cat = None
+    if x is not None or R > 0:
+        _need(x, torch.bfloat16, "x", 2)
+        _shape(x, (M, K), "x")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    else:
+        _need(y, torch.bfloat16, "y", 2)
+        _shape(y, (M, N), "y")
+    need = lora_linear_mxfp4_workspace_size(M, K, N, R)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _same_device(xq, x, xsf, wq, wsf, A_cat, B_cat, y, workspace)
+    if M == 0:
+        return y
+    st = _launch(xq.device, lib.lg_lora_linear_mxfp4, _ptr(x), _ptr(xq), _ptr(xsf), _ptr(wq), _ptr(wsf), _ptr(A_cat),
+                 _ptr(B_cat), _ptr(y), M, K, N, R, _ptr(workspace), ws_bytes)
+    _check(st, "lg_lora_linear_mxfp4")
+    return y
+
+
+def _norm_args(h, post, pre, segment_tokens):
+    """(M, D, segment_tokens, S) of a block-norm call, its kinds checked."""
+    if not isinstance(h, torch.Tensor) or h.dtype not in _STREAM:
+        raise TypeError("the stream must be a bfloat16 or float32 torch.Tensor")
+    _need(h, h.dtype, "the stream", 2)
+    for kind, name in ((post, "post"), (pre, "pre")):
+        if kind not in _NORM:
+            raise ValueError(f"{name} must be None, 'rms' or 'layer', got {kind!r}")
+    M, D = h.shape
+    seg = max(M, 1) if segment_tokens is None else int(segment_tokens)
+    if seg < 1:
+        raise ValueError("segment_tokens must be at least 1")
+    return M, D, seg, -(-M // seg)
+
+
+def _modulation(t, S, D, name):
+    if t is not None:
+        _need(t, torch.float32, name, 2)
+        _shape(t, (S, D), name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6, post="rms", pre="rms",
+               segment_tokens=None, quant=None, h_out=None, n=None, q=None):
+    """The norms between two blocks, with the gate and the scaled residual:
+
+        h' = alpha h + gate * N_post(b),   n = N_pre(h') (1 + scale) + shift
+
+    h [M, D] is the residual stream (bf16 or FP32), b [M, D] bf16 the block's
+    output; gate, scale, shift FP32 [S, D] hold one row per segment of
+    segment_tokens rows (default: one segment).  post and pre are "rms",
+    "layer" or None; b None (the norm that opens a network) needs post None.
+    quant "mxfp8" or "mxfp4" also quantizes n, as mx_quantize(n) or
+    mxfp4_quantize(n) would.  Returns (h', n, (codes, scales)); h' is h itself
+    without b, n is None without pre, the pair is None without quant.  Outputs
+    may be passed in: h_out (h itself updates in place), n, q."""
+    if b is None and post == "rms":
+        post = None  # the default kind has nothing to norm
+    M, D, seg, S = _norm_args(h, post, pre, segment_tokens)
+    if quant not in _CODES:
+        raise ValueError(f"quant must be None, 'mxfp8' or 'mxfp4', got {quant!r}")
+    _modulation(gate, S, D, "gate")
+    _modulation(scale, S, D, "scale")
+    _modulation(shift, S, D, "shift")
+    dev = h.device
+    if b is not None:
+        _need(b, torch.bfloat16, "b", 2)
+        _shape(b, (M, D), "b")
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        else:
+            _need(h_out, h.dtype, "h_out", 2)
+            _shape(h_out, (M, D), "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out needs b: without a block's output the stream stays as it is")
+    if pre is not None and n is None:
+        n = torch.empty((M, D), dtype=torch.bfloat16, device=dev)
+    elif n is not None:
+        _need(n, torch.bfloat16, "n", 2)
+        _shape(n, (M, D), "n")
+    codes = scales = None
+    if quant is not None:
+        width = D if quant == "mxfp8" else D // 2
+        nscales = mx_scale_bytes(M, D)
+        if q is None:
+            q = (torch.empty((M, width), dtype=torch.uint8, device=dev),
+                 torch.empty(nscales, dtype=torch.uint8, device=dev))
+        codes, scales = q
+        _need(codes, torch.uint8, "codes", 2)
+        _shape(codes, (M, width), "codes")
+        _at_least(scales, nscales, "scales")
+    elif q is not None:
+        raise ValueError("q needs quant")
+    _same_device(h, b, gate, scale, shift, h_out, n, codes, scales)
+    if M > 0:
+        args = BlockNormArgs(_addr(h), _addr(b), _addr(gate), _addr(scale), _addr(shift), _addr(h_out), _addr(n),
+                             _addr(codes), _addr(scales), M, seg, D, _STREAM[h.dtype], _NORM[post], _NORM[pre],
+                             _CODES[quant], float(alpha), float(eps))
+        _check(_launch(dev, lib.lg_block_norm, ctypes.byref(args)), "lg_block_norm")
+    return (h if b is None else h_out), n, (q if quant is not None else None)
+
+
+def block_norm_backward_workspace_size(M, D, segment_tokens):
+    return int(lib.lg_block_norm_backward_workspace_size(int(M), int(D), int(segment_tokens)))
+
+
+def block_norm_backward(dn, dh_out, h_out, b=None, gate=None, scale=None, alpha=1.0, eps=1e-6, post="rms", pre="rms",
+                        segment_tokens=None, dh=None, db=None, workspace=None):
+    """Gradients of block_norm: dn and dh_out are those of n (bf16; None without
+    pre) and of h' (the stream's type; None for zero), h_out the h' that
+    block_norm returned, the rest its arguments.  Returns (dh, db, dgate,
+    dscale, dshift), the last three FP32 [S, D]; db and dgate are None without
+    b, dscale and dshift without pre.  dh may be dh_out itself."""
+    if b is None and post == "rms":
+        post = None
+    M, D, seg, S = _norm_args(h_out, post, pre, segment_tokens)
+    _modulation(gate, S, D, "gate")
+    _modulation(scale, S, D, "scale")
+    dev = h_out.device
+    if (dn is None) != (pre is None):
+        raise ValueError("dn is given exactly when there is a pre-norm")
+    if dn is not None:
+        _need(dn, torch.bfloat16, "dn", 2)
+        _shape(dn, (M, D), "dn")
+    if dh_out is not None:
+        _need(dh_out, h_out.dtype, "dh_out", 2)
+        _shape(dh_out, (M, D), "dh_out")
+    if dh is None:
+        dh = torch.empty_like(h_out)
+    else:
+        _need(dh, h_out.dtype, "dh", 2)
+        _shape(dh, (M, D), "dh")
+    dgate = dscale = dshift = None
+    if b is not None:
+        _need(b, torch.bfloat16, "b", 2)
+        _shape(b, (M, D), "b")
+        if db is None:
+            db = torch.empty_like(b)
+        else:
+            _need(db, torch.bfloat16, "db", 2)
+            _shape(db, (M, D), "db")
+        dgate = torch.empty((S, D), dtype=torch.float32, device=dev)
+    elif db is not None:
+        raise ValueError("db needs b")
+    if dn is not None:
+        dscale = torch.empty((S, D), dtype=torch.float32, device=dev)
+        dshift = torch.empty((S, D), dtype=torch.float32, device=dev)
+    need = block_norm_backward_workspace_size(M, D, seg)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _same_device(h_out, dn, dh_out, b, gate, scale, dh, db, workspace)
+    if M > 0:
+        args = BlockNormBackwardArgs(_addr(dn), _addr(dh_out), _addr(h_out), _addr(b), _addr(gate), _addr(scale),
+                                     _addr(dh), _addr(db), _addr(dgate), _addr(dscale), _addr(dshift), M, seg, D,
+                                     _STREAM[h_out.dtype], _NORM[post], _NORM[pre], float(alpha), float(eps))
+        _check(_launch(dev, lib.lg_block_norm_backward, ctypes.byref(args), _ptr(workspace), ws_bytes),
+               "lg_block_norm_backward")
+    return dh, db, dgate, dscale, dshift
 
 
 def renoise(up, sigma, seed, offset=0, out=None):

@@ -14,6 +14,7 @@ namespace {
 constexpr uint64_t kDefaultWaitLimitNs = 4000000000ull;
 constexpr int kMaxRank = 576;
 constexpr int kMaxDim = 1 << 20;
+constexpr int kMaxNormDim = 16384;  // a row's values stay in the registers of one CTA
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
@@ -182,6 +183,159 @@ lg_status lg_mx_quantize(const void* in, int64_t rows, int K, void* codes, void*
                   1);
 }
 
+lg_status lg_mxfp4_quantize(const void* in, int64_t rows, int K, void* codes, void* scales, void* stream) {
+  if (rows < 0 || K < 0) return LG_ERR_INVALID_ARG;
+  if (rows >= (int64_t)1 << 31 || K < 128 || K % 128 || K > kMaxDim) return LG_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return LG_OK;
+  if (!in || !codes || !scales) return LG_ERR_INVALID_ARG;
+  if (!aligned16(in) || !aligned16(codes) || !aligned16(scales)) return LG_ERR_MISALIGNED;
+  const uint64_t bi = 2ull * rows * K, bc = rows * (uint64_t)(K / 2), bs = lg_mx_scale_bytes(rows, K);
+  if (overlaps(in, bi, codes, bc) || overlaps(in, bi, scales, bs) || overlaps(codes, bc, scales, bs))
+    return LG_ERR_INVALID_ARG;
+  int sms = 0;
+  lg_status st = current_device(&sms);
+  if (st != LG_OK) return st;
+  return launched(lg::launch_mxfp4_quantize(reinterpret_cast<const uint16_t*>(in), rows, K,
+                                            reinterpret_cast<uint8_t*>(codes), reinterpret_cast<uint8_t*>(scales),
+                                            sms, as_stream(stream)),
+                  1);
+}
+
+lg_status lg_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int K, void* out, void* stream) {
+  if (rows < 0 || K < 0) return LG_ERR_INVALID_ARG;
+  if (rows >= (int64_t)1 << 31 || K < 128 || K % 128 || K > kMaxDim) return LG_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return LG_OK;
+  if (!codes || !scales || !out) return LG_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return LG_ERR_MISALIGNED;
+  const uint64_t bo = 2ull * rows * K, bc = rows * (uint64_t)(K / 2), bs = lg_mx_scale_bytes(rows, K);
+  if (overlaps(out, bo, codes, bc) || overlaps(out, bo, scales, bs)) return LG_ERR_INVALID_ARG;
+  int sms = 0;
+  lg_status st = current_device(&sms);
+  if (st != LG_OK) return st;
+  return launched(lg::launch_mxfp4_dequantize(reinterpret_cast<const uint8_t*>(codes),
+                                              reinterpret_cast<const uint8_t*>(scales), rows, K,
+                                              reinterpret_cast<uint16_t*>(out), sms, as_stream(stream)),
+                  1);
+}
+
+namespace {
+
+// A buffer of a block-norm call; bytes 0 (or a null pointer) overlaps nothing.
+struct Buffer {
+  const void* p;
+  uint64_t bytes;
+};
+
+// Alignment of every buffer, then every output against every other buffer
+// (out[0] may be in[0] itself).
+lg_status check_buffers(const Buffer* in, int n_in, const Buffer* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].p && !aligned16(in[i].p)) return LG_ERR_MISALIGNED;
+  for (int i = 0; i < n_out; ++i)
+    if (out[i].p && !aligned16(out[i].p)) return LG_ERR_MISALIGNED;
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i].p || !out[i].bytes) continue;
+    for (int j = 0; j < n_in; ++j) {
+      if (i == 0 && j == 0 && in[0].p == out[0].p) continue;
+      if (in[j].p && in[j].bytes && overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return LG_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && out[j].bytes && overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return LG_ERR_INVALID_ARG;
+  }
+  return LG_OK;
+}
+
+bool norm_kind_ok(int k) { return k == LG_NORM_NONE || k == LG_NORM_RMS || k == LG_NORM_LAYER; }
+
+lg_status check_norm_shape(int64_t M, int64_t segment_tokens, int D, int stream_type, int post, int pre, float alpha,
+                           float eps) {
+  if (M < 0 || D < 0 || segment_tokens < 1) return LG_ERR_INVALID_ARG;
+  if (M >= (int64_t)1 << 31 || D < 8 || D % 8 || D > kMaxNormDim) return LG_ERR_UNSUPPORTED_SHAPE;
+  if (stream_type != LG_STREAM_BF16 && stream_type != LG_STREAM_FP32) return LG_ERR_INVALID_ARG;
+  if (!norm_kind_ok(post) || !norm_kind_ok(pre)) return LG_ERR_INVALID_ARG;
+  if (!std::isfinite(alpha) || !std::isfinite(eps) || !(eps > 0.0f)) return LG_ERR_INVALID_ARG;
+  return LG_OK;
+}
+
+}  // namespace
+
+lg_status lg_block_norm(const lg_block_norm_args* a, void* stream) {
+  if (!a) return LG_ERR_INVALID_ARG;
+  lg_status st = check_norm_shape(a->M, a->segment_tokens, a->D, a->stream_type, a->post, a->pre, a->alpha, a->eps);
+  if (st != LG_OK) return st;
+  if (a->codes_format != LG_CODES_NONE && a->codes_format != LG_CODES_MXFP8 && a->codes_format != LG_CODES_MXFP4)
+    return LG_ERR_INVALID_ARG;
+  const bool codes = a->codes_format != LG_CODES_NONE;
+  if (codes && a->D % 128) return LG_ERR_UNSUPPORTED_SHAPE;
+  if (!a->h || (codes ? (!a->codes || !a->scales) : (a->codes || a->scales))) return LG_ERR_INVALID_ARG;
+  if (a->b ? !a->h_out : (a->h_out || a->gate || a->post != LG_NORM_NONE || a->alpha != 1.0f))
+    return LG_ERR_INVALID_ARG;
+  if (a->pre == LG_NORM_NONE) {
+    if (!a->b || a->n || codes || a->scale || a->shift) return LG_ERR_INVALID_ARG;
+  } else if (!a->n && !codes) {
+    return LG_ERR_INVALID_ARG;
+  }
+  const uint64_t n = (uint64_t)a->M * a->D, S = ((uint64_t)a->M + a->segment_tokens - 1) / a->segment_tokens;
+  const uint64_t bs = n * (a->stream_type == LG_STREAM_FP32 ? 4 : 2), bm = 4ull * S * a->D;
+  const Buffer in[5] = {{a->h, bs}, {a->b, 2 * n}, {a->gate, bm}, {a->scale, bm}, {a->shift, bm}};
+  const Buffer out[4] = {{a->h_out, bs},
+                         {a->n, 2 * n},
+                         {a->codes, a->codes_format == LG_CODES_MXFP4 ? n / 2 : n},
+                         {a->scales, codes ? lg_mx_scale_bytes(a->M, a->D) : 0}};
+  st = check_buffers(in, 5, out, 4);
+  if (st != LG_OK || a->M == 0) return st;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != LG_OK) return st;
+  const lg::BlockNormLaunch p{a->h,      a->b,     a->gate,   a->scale, a->shift,
+                              a->h_out,  a->n,     a->codes,  a->scales, a->M,
+                              a->segment_tokens,   a->D,      a->stream_type == LG_STREAM_FP32,
+                              a->post,   a->pre,   a->codes_format, a->alpha, a->eps};
+  return launched(lg::launch_block_norm(p, as_stream(stream)), 1);
+}
+
+size_t lg_block_norm_backward_workspace_size(int64_t M, int D, int64_t segment_tokens) {
+  if (M < 1 || M >= (int64_t)1 << 31 || D < 8 || D % 8 || D > kMaxNormDim || segment_tokens < 1) return 0;
+  int64_t per = 0;
+  return (size_t)lg::block_norm_backward_chunks(M, segment_tokens, &per) * 3 * D * sizeof(float);
+}
+
+lg_status lg_block_norm_backward(const lg_block_norm_backward_args* a, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  if (!a) return LG_ERR_INVALID_ARG;
+  lg_status st = check_norm_shape(a->M, a->segment_tokens, a->D, a->stream_type, a->post, a->pre, a->alpha, a->eps);
+  if (st != LG_OK) return st;
+  if ((a->pre != LG_NORM_NONE) != (a->dn != nullptr)) return LG_ERR_INVALID_ARG;
+  if (!a->dn && (!a->dh_out || a->scale || a->dscale || a->dshift)) return LG_ERR_INVALID_ARG;
+  if (!a->h_out) return LG_ERR_INVALID_ARG;
+  if (!a->b && (a->gate || a->db || a->dgate || a->post != LG_NORM_NONE || a->alpha != 1.0f)) return LG_ERR_INVALID_ARG;
+  if (!a->dh && !a->db && !a->dgate && !a->dscale && !a->dshift) return LG_ERR_INVALID_ARG;
+  const size_t need = lg_block_norm_backward_workspace_size(a->M, a->D, a->segment_tokens);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need) return LG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return LG_ERR_MISALIGNED;
+  }
+  const uint64_t n = (uint64_t)a->M * a->D, S = ((uint64_t)a->M + a->segment_tokens - 1) / a->segment_tokens;
+  const uint64_t bs = n * (a->stream_type == LG_STREAM_FP32 ? 4 : 2), bm = 4ull * S * a->D;
+  const Buffer in[6] = {{a->dh_out, bs}, {a->dn, 2 * n}, {a->h_out, bs}, {a->b, 2 * n}, {a->gate, bm}, {a->scale, bm}};
+  const Buffer out[6] = {{a->dh, bs},     {a->db, 2 * n},  {a->dgate, bm},
+                         {a->dscale, bm}, {a->dshift, bm}, {need > 0 ? workspace : nullptr, need}};
+  st = check_buffers(in, 6, out, 6);
+  if (st != LG_OK || a->M == 0) return st;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != LG_OK) return st;
+  const lg::BlockNormBackwardLaunch p{a->dn,     a->dh_out, a->h_out,  a->b,      a->gate, a->scale,
+                                      a->dh,     a->db,     a->dgate,  a->dscale, a->dshift,
+                                      reinterpret_cast<float*>(workspace),
+                                      a->M,      a->segment_tokens,    a->D,      a->stream_type == LG_STREAM_FP32,
+                                      a->post,   a->pre,    a->alpha,  a->eps};
+  int kernels = 0;
+  const cudaError_t e = lg::launch_block_norm_backward(p, &kernels, as_stream(stream));
+  return launched(e, (uint64_t)kernels);
+}
+
 namespace {
 // bf16 copies of A_cat [R, K] and B_cat [N, R], each padded to 256 bytes.
 size_t factor_copy_bytes(int K, int N, int R) { return (size_t)(align256(2ull * R * K) + align256(2ull * N * R)); }
@@ -203,8 +357,9 @@ size_t lg_lora_linear_euler_workspace_size(int64_t M, int K, int N, int R) {
 
 namespace {
 
-// MXFP8 operands of lg_lora_linear_mxfp8 (null for the bf16 layer).
+// Operands of lg_lora_linear_mxfp8 / _mxfp4 (null for the bf16 layer).
 struct MxOperands {
+  int bits;  // 8: E4M3 codes, one byte each; 4: E2M1 codes, two per byte
   const void* xq;
   const void* xsf;
   const void* wq;
@@ -248,7 +403,9 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
     if (!aligned16(eu->z) || (eu->z_bf16 && !aligned16(eu->z_bf16))) return LG_ERR_MISALIGNED;
   }
   const bool no_y = sw || eu;
-  if (!x || (!no_y && !y) || (!mx && !W)) return LG_ERR_INVALID_ARG;
+  // The 4-bit layer reads x for the LoRA term alone.
+  const bool need_x = !(mx && mx->bits == 4 && R == 0);
+  if ((need_x && !x) || (!no_y && !y) || (!mx && !W)) return LG_ERR_INVALID_ARG;
   if (mx && (!mx->xq || !mx->xsf || !mx->wq || !mx->wsf)) return LG_ERR_INVALID_ARG;
   if (R > 0 && (!A_cat || !B_cat)) return LG_ERR_INVALID_ARG;
   if (!aligned16(x) || (!no_y && !aligned16(y)) || (!mx && !aligned16(W))) return LG_ERR_MISALIGNED;
@@ -260,7 +417,8 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
     if (!workspace || ws_bytes < need) return LG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LG_ERR_MISALIGNED;
   }
-  const uint64_t bx = 2ull * M * K, bw = 2ull * N * K;
+  const uint64_t bx = x ? 2ull * M * K : 0, bw = 2ull * N * K;
+  const uint64_t bxq = mx ? (uint64_t)M * K * mx->bits / 8 : 0, bwq = mx ? (uint64_t)N * K * mx->bits / 8 : 0;
   // The output region: y, the SwiGLU codes and scales, or the latent z (and
   // its bf16 copy, checked here).
   const void* out = sw ? sw->codes : (eu ? eu->z : y);
@@ -275,14 +433,14 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   if (sw && M > 0) {
     const uint64_t bs = lg_mx_scale_bytes(M, N / 2);
     if (overlaps(sw->codes, by, sw->scales, bs) || overlaps(sw->scales, bs, x, bx) ||
-        overlaps(sw->scales, bs, mx->xq, 1ull * M * K) || overlaps(sw->scales, bs, mx->wq, 1ull * N * K) ||
+        overlaps(sw->scales, bs, mx->xq, bxq) || overlaps(sw->scales, bs, mx->wq, bwq) ||
         (R > 0 && overlaps(sw->scales, bs, workspace, need)))
       return LG_ERR_INVALID_ARG;
   }
   y = const_cast<void*>(out);
   if (M > 0) {
     if (overlaps(y, by, x, bx) || (!mx && overlaps(y, by, W, bw))) return LG_ERR_INVALID_ARG;
-    if (mx && (overlaps(y, by, mx->xq, 1ull * M * K) || overlaps(y, by, mx->wq, 1ull * N * K) ||
+    if (mx && (overlaps(y, by, mx->xq, bxq) || overlaps(y, by, mx->wq, bwq) ||
                overlaps(y, by, mx->xsf, lg_mx_scale_bytes(M, K)) || overlaps(y, by, mx->wsf, lg_mx_scale_bytes(N, K))))
       return LG_ERR_INVALID_ARG;
     if (R > 0 && (overlaps(y, by, A_cat, 4ull * R * K) || overlaps(y, by, B_cat, 4ull * N * R) ||
@@ -291,6 +449,11 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   }
   if (R > 0 && (overlaps(workspace, need, A_cat, 4ull * R * K) || overlaps(workspace, need, B_cat, 4ull * N * R) ||
                 overlaps(workspace, need, x, bx) || (!mx && overlaps(workspace, need, W, bw))))
+    return LG_ERR_INVALID_ARG;
+  if (R > 0 && mx && mx->bits == 4 &&
+      (overlaps(workspace, need, mx->xq, bxq) || overlaps(workspace, need, mx->wq, bwq) ||
+       overlaps(workspace, need, mx->xsf, lg_mx_scale_bytes(M, K)) ||
+       overlaps(workspace, need, mx->wsf, lg_mx_scale_bytes(N, K))))
     return LG_ERR_INVALID_ARG;
   if (M == 0) return LG_OK;
   int sms = 0;
@@ -318,7 +481,7 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   p.sm_count = sms;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   if (mx) {
-    p.mx = true;
+    p.mx_bits = mx->bits;
     p.xq = mx->xq;
     p.xsf = mx->xsf;
     p.wq = mx->wq;
@@ -389,7 +552,19 @@ lg_status lg_lora_linear(const void* x, const void* W, const float* A_cat, const
 lg_status lg_lora_linear_mxfp8(const void* x, const void* x_codes, const void* x_scales, const void* W_codes,
                                const void* W_scales, const float* A_cat, const float* B_cat, void* y, int64_t M,
                                int K, int N, int R, void* workspace, size_t ws_bytes, void* stream) {
-  const MxOperands mx{x_codes, x_scales, W_codes, W_scales};
+  const MxOperands mx{8, x_codes, x_scales, W_codes, W_scales};
+  return lora_linear_impl(x, nullptr, A_cat, B_cat, y, M, K, N, R, workspace, ws_bytes, stream, &mx);
+}
+
+size_t lg_lora_linear_mxfp4_workspace_size(int64_t M, int K, int N, int R) {
+  if (K % 128) return 0;
+  return lg_lora_linear_workspace_size(M, K, N, R);
+}
+
+lg_status lg_lora_linear_mxfp4(const void* x, const void* x_codes, const void* x_scales, const void* W_codes,
+                               const void* W_scales, const float* A_cat, const float* B_cat, void* y, int64_t M,
+                               int K, int N, int R, void* workspace, size_t ws_bytes, void* stream) {
+  const MxOperands mx{4, x_codes, x_scales, W_codes, W_scales};
   return lora_linear_impl(x, nullptr, A_cat, B_cat, y, M, K, N, R, workspace, ws_bytes, stream, &mx);
 }
 
@@ -399,7 +574,7 @@ lg_status lg_lora_linear_swiglu_mxfp8(const void* x, const void* x_codes, const 
                                       size_t ws_bytes, void* stream) {
   if (F < 0 || F > kMaxDim / 2) return LG_ERR_UNSUPPORTED_SHAPE;
   if (F % 128) return LG_ERR_UNSUPPORTED_SHAPE;
-  const MxOperands mx{x_codes, x_scales, W_codes, W_scales};
+  const MxOperands mx{8, x_codes, x_scales, W_codes, W_scales};
   const SwigluOut sw{out_codes, out_scales};
   return lora_linear_impl(x, nullptr, A_cat, B_cat, nullptr, M, K, 2 * F, R, workspace, ws_bytes, stream, &mx, &sw);
 }

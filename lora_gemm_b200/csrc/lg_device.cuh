@@ -502,6 +502,30 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3(int m, int n, uint32_t sf_a
          | (sf_a << 29);                 // A scale-factor ID
 }
 
+// Block-scaled MXFP4 MMA (packed E2M1 A and B in shared memory, one E8M0 scale
+// per 32 values along K in tensor memory), SM pair: D[M=256, N] (+)= (A x sfa)
+// (B x sfb)^T over K = 64, two scale bytes per row.
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+// Instruction descriptor, kind::mxf4: E2M1 A and B (both K-major), E8M0 scale
+// factors, dense K = 64; sf_a / sf_b (0 or 2) select the first of the two
+// bytes of the 32-bit scale word each row's scales are taken from.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_a, uint32_t sf_b) {
+  return (sf_b << 4)                      // B scale-factor ID
+         | (1u << 7) | (1u << 10)        // A, B format: E2M1
+         | ((uint32_t)(n >> 3) << 17)    // N / 8
+         | (1u << 23)                    // scale format: E8M0
+         | ((uint32_t)(m >> 7) << 27)    // M / 128
+         | (sf_a << 29);                 // A scale-factor ID
+}
 // Shared-memory descriptor of 32 rows of 16 bytes stored contiguously, no
 // swizzle (four 8-row core matrices 128 bytes apart): the source layout of a
 // tcgen05.cp 32x128b copy.

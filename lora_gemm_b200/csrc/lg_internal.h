@@ -46,6 +46,57 @@ cudaError_t launch_prep_bf16(const float* A_cat, const float* B_cat, uint16_t* d
 cudaError_t launch_mx_quantize(const uint16_t* in, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
                                int sm_count, cudaStream_t s);
 
+// MXFP4 quantization of bf16 rows [rows, K] along K (K % 128 == 0): packed
+// E2M1 codes [rows, K / 2] and E8M0 scales in the blocked layout; and back.
+cudaError_t launch_mxfp4_quantize(const uint16_t* in, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                                  int sm_count, cudaStream_t s);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, uint16_t* out,
+                                    int sm_count, cudaStream_t s);
+
+// Block norms; fields as in lg_block_norm_args / lg_block_norm_backward_args.
+struct BlockNormLaunch {
+  const void* h;
+  const void* b;
+  const float* gate;
+  const float* scale;
+  const float* shift;
+  void* h_out;
+  void* n;
+  void* codes;
+  void* scales;
+  int64_t M, segment_tokens;
+  int D;
+  bool fp32;
+  int post, pre, codes_format;
+  float alpha, eps;
+};
+cudaError_t launch_block_norm(const BlockNormLaunch& p, cudaStream_t s);
+
+struct BlockNormBackwardLaunch {
+  const void* dn;
+  const void* dh_out;
+  const void* h_out;
+  const void* b;
+  const float* gate;
+  const float* scale;
+  void* dh;
+  void* db;
+  float* dgate;
+  float* dscale;
+  float* dshift;
+  float* workspace;
+  int64_t M, segment_tokens;
+  int D;
+  bool fp32;
+  int post, pre;
+  float alpha, eps;
+};
+// Chunks of rows the backward pass works in (each holds 3 D partial sums in
+// the workspace), and how many a full segment has.
+int64_t block_norm_backward_chunks(int64_t M, int64_t segment_tokens, int64_t* per_segment);
+// *kernels: launches made.
+cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* kernels, cudaStream_t s);
+
 // Merged-LoRA linear (tcgen05 kernel).  Factors already in bf16.
 struct LinearLaunch {
   const void* x;
@@ -57,10 +108,11 @@ struct LinearLaunch {
   int K, N, R;
   int sm_count;
   uint64_t wait_limit_ns;
-  // MXFP8 base term (lg_lora_linear_mxfp8): E4M3 codes and blocked E8M0
-  // scales of x [M, K] and W [N, K]; x above stays the bf16 activations (the
-  // LoRA path reads them), W is unused.
-  bool mx = false;
+  // MX base term: E4M3 codes (mx_bits 8, lg_lora_linear_mxfp8) or packed E2M1
+  // codes (mx_bits 4, lg_lora_linear_mxfp4) and blocked E8M0 scales of x
+  // [M, K] and W [N, K]; x above stays the bf16 activations (the LoRA path
+  // reads them), W is unused.
+  int mx_bits = 0;
   const void* xq = nullptr;
   const void* xsf = nullptr;
   const void* wq = nullptr;

@@ -29,6 +29,7 @@ Sources (the pages are cited by title and section):
 * MXFP8: Open Compute Project, "OCP Microscaling Formats (MX) v1.0" and "OCP
   8-bit Floating Point (OFP8)" (the pages only name MXFP8 linear layers,
   section "Where the 3.9x speedup comes from" of the English article).
+* MXFP4: the same MX specification's 4-bit format (E2M1 elements).
 
 Pins (tests/test_oracle_*.py, run with ``-m "not gpu"``):
 
@@ -51,8 +52,13 @@ Pins (tests/test_oracle_*.py, run with ``-m "not gpu"``):
                  saturation, the block-exponent definition, the 3-bit-mantissa
                  error bound and brute-force loops on a tiny layer; SiLU
                  against PyTorch's and its limits, SwiGLU by brute force.
+* mxfp4       -- the E2M1 grid, round-to-nearest-even at every midpoint,
+                 saturation, block exponents, blocks with a NaN or an infinity,
+                 the packed layout and brute-force loops on a tiny layer.
+* norm        -- the formulas by loops and every gradient against central
+                 differences.
 
 Every function here has a pin; none is "parity unpinned".
 """
 
-from . import flow, lora, mxfp8, noise, philox  # noqa: F401
+from . import flow, lora, mxfp4, mxfp8, noise, norm, philox  # noqa: F401

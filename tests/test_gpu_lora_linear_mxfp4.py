@@ -1,0 +1,133 @@
+"""GPU parity of lora_linear_mxfp4 with the FP64 oracle.
+
+Without adapters the product of MXFP4 values is exact up to FP32 accumulation
+and the rounding of y to bf16: |y - ref| <= 2^-8 |ref| + K 2^-24 sum|products|
+(each of the K terms may cost half an FP32 step of the running sum).  With
+adapters the bf16 layer's bar applies (bf16 factors, bf16 h): relative
+Frobenius error 1e-2, as for the other layers."""
+
+import numpy as np
+import pytest
+import torch
+
+import lora_gemm_b200 as lg
+from oracle import mxfp4 as o4
+from tests.util import rel_fro
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL = 1e-2
+
+
+def _np64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _layer(M, K, N, R, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(M, K, generator=g) * torch.exp2(torch.randn(M, 1, generator=g))).to(torch.bfloat16)
+    W = (torch.randn(N, K, generator=g) * K ** -0.5).to(torch.bfloat16)
+    A = (torch.randn(R, K, generator=g) * K ** -0.5).to(DEV) if R else None
+    B = (torch.randn(N, R, generator=g) * 0.1).to(DEV) if R else None
+    return x.to(DEV), W.to(DEV), A, B
+
+
+def _run(x, W, A, B, **kw):
+    y = lg.lora_linear_mxfp4(x, lg.mxfp4_quantize(x), lg.mxfp4_quantize(W), A, B, **kw)
+    assert lg.get_last_device_error() == lg.LG_OK
+    return y
+
+
+def _check_base(y, x, W):
+    xq, wq = o4.quantized(_np64(x)), o4.quantized(_np64(W))
+    ref, mag = xq @ wq.T, np.abs(xq) @ np.abs(wq).T
+    # Plus 2^-126, FP32's smallest normal number: a product of a row scaled by
+    # 2^-120 with a column scaled by 2^-60 is near 2^-180, and neither the FP32
+    # accumulator nor bf16 (smallest value 2^-133) can hold it.
+    bad = np.abs(_np64(y) - ref) > 2.0 ** -8 * np.abs(ref) + x.shape[1] * 2.0 ** -24 * mag + 2.0 ** -126
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:5])
+
+
+BASE = [(1, 128, 32), (2, 256, 96), (7, 384, 64), (8, 1024, 320), (17, 640, 256), (33, 1152, 288), (64, 512, 1024),
+        (65, 7168, 96), (129, 128, 256), (256, 256, 256), (257, 384, 544), (700, 896, 1024), (1, 28672, 64)]
+
+
+@pytest.mark.parametrize("M,K,N", BASE)
+def test_base_term_elementwise(M, K, N):
+    x, W, _, _ = _layer(M, K, N, 0, seed=M + 3 * K + N)
+    _check_base(_run(x, W, None, None), x, W)
+
+
+@pytest.mark.parametrize("M,K,N,R", [(1, 128, 64, 64), (3, 256, 32, 576), (16, 1024, 1024, 192), (48, 384, 320, 576),
+                                     (130, 7168, 256, 576), (517, 384, 320, 576), (1000, 1024, 896, 64),
+                                     (2304, 1024, 1024, 576), (1, 7168, 7168, 576)])
+def test_with_adapters(M, K, N, R):
+    x, W, A, B = _layer(M, K, N, R, seed=M + 3 * K + N)
+    ref = o4.lora_linear_mxfp4(_np64(x), _np64(W), _np64(A), _np64(B))
+    y = _np64(_run(x, W, A, B))
+    assert rel_fro(y, ref) <= TOL
+    assert np.linalg.norm(y - ref, axis=1).max() <= 2 * TOL * np.linalg.norm(ref, axis=1).max()
+
+
+@pytest.mark.parametrize("G", [2, 4, 8])
+def test_cluster_sizes(G):
+    """Several SM pairs per panel; 896 is an odd number of scale groups, so sweeps in both directions meet the half stage."""
+    x, W, A, B = _layer(37 * 256 + 5, 896, 1792, 576, seed=G)
+    lg.set_cluster_size(G)
+    try:
+        y, y0 = _run(x, W, A, B), _run(x, W, None, None)
+    finally:
+        lg.set_cluster_size(0)
+    rows = np.r_[0:300, 9000:9477]
+    idx = torch.as_tensor(rows, device=DEV)
+    ref = o4.lora_linear_mxfp4(_np64(x[idx]), _np64(W), _np64(A), _np64(B))
+    assert rel_fro(_np64(y[idx]), ref) <= TOL
+    _check_base(y0[idx], x[idx], W)
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_extreme_scales_and_nan_blocks(M):
+    """Rows and columns at both ends of the scale range; a NaN block makes its row (column) NaN and no other."""
+    x, W, _, _ = _layer(M, 512, 128, 0, seed=3)
+    x, W = x.clone(), W.clone()
+    x[0] *= 2.0 ** 60
+    x[1] *= 2.0 ** -120
+    W[1] *= 2.0 ** 60
+    W[2] *= 2.0 ** -60
+    _check_base(_run(x, W, None, None), x, W)
+    x[2, 77], W[3, 500] = float("nan"), float("inf")
+    y = _run(x, W, None, None)
+    nan = torch.zeros(M, 128, dtype=torch.bool)
+    nan[2], nan[:, 3] = True, True
+    assert torch.equal(torch.isnan(y).cpu(), nan)
+    assert torch.isfinite(y.cpu()[~nan]).all()
+
+
+def test_rows_behind_the_last_token_stay():
+    """y is a slice of a larger buffer: the rows behind it keep their contents, also where the tile passes them."""
+    for M in (3, 200):
+        x, W, A, B = _layer(M, 256, 64, 64, seed=M)
+        buf = torch.full((M + 64, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+        _run(x, W, A, B, y=buf[:M])
+        assert (buf[M:] == 5.0).all()
+        assert torch.equal(buf[:M], _run(x, W, A, B))
+
+
+def test_x_is_not_needed_without_adapters():
+    x, W, _, _ = _layer(40, 256, 64, 0, seed=2)
+    y = lg.lora_linear_mxfp4(None, lg.mxfp4_quantize(x), lg.mxfp4_quantize(W), None, None)
+    assert torch.equal(y, _run(x, W, None, None))
+    assert lg.lora_linear_mxfp4(None, lg.mxfp4_quantize(x[:0]), lg.mxfp4_quantize(W), None, None).shape == (0, 64)
+
+
+def test_wait_timeout_is_reported():
+    x, W, A, B = _layer(2048, 1024, 1792, 576, seed=19)
+    lg.set_wait_limit_ns(1)
+    try:
+        lg.lora_linear_mxfp4(x, lg.mxfp4_quantize(x), lg.mxfp4_quantize(W), A, B)
+        status = lg.get_last_device_error()
+    finally:
+        lg.set_wait_limit_ns(0)
+    assert status == lg.LG_ERR_DEVICE_TIMEOUT
+    ref = o4.lora_linear_mxfp4(_np64(x), _np64(W), _np64(A), _np64(B))
+    assert rel_fro(_np64(_run(x, W, A, B)), ref) <= TOL
