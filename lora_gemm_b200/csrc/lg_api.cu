@@ -297,8 +297,7 @@ lg_status lg_block_norm(const lg_block_norm_args* a, void* stream) {
 
 size_t lg_block_norm_backward_workspace_size(int64_t M, int D, int64_t segment_tokens) {
   if (M < 1 || M >= (int64_t)1 << 31 || D < 8 || D % 8 || D > kMaxNormDim || segment_tokens < 1) return 0;
-  int64_t per = 0;
-  return (size_t)lg::block_norm_backward_chunks(M, segment_tokens, &per) * 3 * D * sizeof(float);
+  return lg::block_norm_backward_workspace(M, D, segment_tokens);
 }
 
 lg_status lg_block_norm_backward(const lg_block_norm_backward_args* a, void* workspace, size_t ws_bytes,

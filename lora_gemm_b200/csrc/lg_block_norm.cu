@@ -13,8 +13,8 @@
 // reads again (more than the row itself), and that the rows resident on an SM
 // share there.
 //
-// Backward: with u = N_post(b), x^ = N_pre(h'), r the reciprocal deviation of
-// a norm and g its output's gradient, the input's gradient is
+// Backward: with x^ a normalised row, r its reciprocal deviation and g the
+// gradient there, the input's gradient is
 //
 //   RMS:    r (g - x^ mean(g x^))
 //   layer:  r (g - mean g - x^ mean(g x^))
@@ -288,6 +288,12 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Backward.
+// ---------------------------------------------------------------------------
+constexpr int kBackStagesMax = 4;
+constexpr size_t kBackSmem = 200 * 1024;  // for the row stages, of the 227 KB a CTA may have
+
 struct BackArgs {
   const void* dn;
   const void* dh_out;
@@ -297,26 +303,133 @@ struct BackArgs {
   const float* scale;
   void* dh;
   void* db;
-  float* sums;        // [chunks][3][D] partials (dgate, dscale, dshift)
+  float* sums[3];     // dgate, dscale, dshift: rows of `sum_stride` floats, one per chunk (or per segment, direct)
+  int64_t sum_stride;
   int64_t M;
   int64_t seg;
-  int64_t seg_chunks;   // chunks per segment
+  int64_t seg_chunks;   // chunks of a full segment; the last segment may have fewer
+  int64_t segments;
   int64_t chunk_rows;
-  int D, post, pre;
+  int D, post, pre, stages;
   float alpha, eps;
 };
 
-template <bool FP32, int CH>
-__global__ void __launch_bounds__(1024) k_block_norm_backward(const BackArgs a) {
-  __shared__ float slots[2][8][kMaxWarps];  // alternating rows: a row's last reads and the next row's writes
-  const int warps = (int)blockDim.x >> 5;
-  const int T = (int)blockDim.x;
-  const int64_t s = blockIdx.x / a.seg_chunks;
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most n (0 .. 3) of this thread's newest groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Sums of N = 8 or 16 values over all threads of the CTA, in every thread.
+// Within a warp each step exchanges half of the values a lane still holds with
+// the lane whose bit differs (9 shuffles for 8 values instead of 40): value i
+// ends in lanes i * 32 / N and up.  `slot` [N][kMaxWarps] is not written again
+// before the CTA's next but one call.
+template <int N>
+__device__ __forceinline__ void cta_sums(float (&v)[N], int warps, float (*slot)[kMaxWarps]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int half = N / 2;
+#pragma unroll
+  for (int bit = 16; bit > 0; bit >>= 1) {
+    if (half >= 1) {
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < half) {
+          const float give = up ? v[i] : v[i + half];
+          const float keep = up ? v[i + half] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
+      }
+      half >>= 1;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+    }
+  }
+  constexpr int kLanes = 32 / N;  // lanes that share a value
+  float total = v[0];
+  if (warps > 1) {
+    const int idx = lane / kLanes, sub = lane % kLanes;
+    if (sub == 0) slot[idx][warp] = total;
+    __syncthreads();
+    total = 0.f;
+    for (int w = sub; w < warps; w += kLanes) total += slot[idx][w];
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, total, i * kLanes);
+}
+
+// One CTA: consecutive rows of one segment; thread t always has columns
+// [8 (c T + t), + 8).  Rows arrive through a ring of shared-memory stages
+// filled by cp.async: every thread copies and reads its own 16-byte pieces, so
+// the ring needs no barrier, and the rows in flight cost no registers (which
+// hold the three column sums).
+//
+// All row sums come from one pass (two with a layer norm, whose means are
+// taken first so that the squares are those of centred values).  With x, b the
+// centred rows (RMS: the rows), g = dn (1 + scale), t = gate:
+//   rx^2 = D / sum x^2, ru^2 = D / sum b^2 (+ eps),   k = rx^3 mean(g x)
+//   dh' = dh_out + rx (g - mean g) - k x,   w = t dh',  u = ru b
+//   sum w u = ru (sum t b dh_out + rx (sum t b g - mean g sum t b) - k sum t b x)
+//   sum w   =     sum t dh_out   + rx (sum t g   - mean g sum t)   - k sum t x
+//   db = ru (w - mean w - u mean(w u))
+// so the second norm's sums need no second pass over the first one's result.
+template <bool FP32, int CH, bool LAYER>
+__global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward(const BackArgs a) {
+  constexpr int N = LAYER ? 16 : 8;
+  constexpr int W = FP32 ? 2 : 1;              // 16-byte pieces of eight stream values
+  constexpr int PIECES = 2 * W + 2;            // h, dh_out, dn, b
+  extern __shared__ uint4 ring[];              // [stages][CH][PIECES][T]
+  __shared__ float slots[2][N][kMaxWarps];
+  __shared__ float mean_slots[2][8][kMaxWarps];
+  const int T = (int)blockDim.x, warps = T >> 5, t = (int)threadIdx.x;
+  int64_t s = blockIdx.x / a.seg_chunks;
+  if (s >= a.segments) s = a.segments - 1;
   const int64_t first = s * a.seg + (blockIdx.x - s * a.seg_chunks) * a.chunk_rows;
   int64_t last = first + a.chunk_rows;
   if (last > (s + 1) * a.seg) last = (s + 1) * a.seg;
   if (last > a.M) last = a.M;
   const float inv_d = 1.0f / (float)a.D;
+  const float* gate = a.gate ? a.gate + s * a.D : nullptr;
+  const float* scale = a.scale ? a.scale + s * a.D : nullptr;
+  bool live[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) live[c] = (c * T + t) * 8 < a.D;
+
+  auto piece = [&](int stage, int c, int k) { return &ring[((stage * CH + c) * PIECES + k) * T + t]; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < last) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (!live[c]) continue;
+        const int64_t at = row * a.D + (c * T + t) * 8;
+        if (a.dn) {
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            cp_async16(smem_addr(piece(stage, c, w)), reinterpret_cast<const uint8_t*>(a.h) + at * (2 * W) + 16 * w);
+          cp_async16(smem_addr(piece(stage, c, 2 * W)), reinterpret_cast<const uint8_t*>(a.dn) + at * 2);
+        }
+        if (a.dh_out) {
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            cp_async16(smem_addr(piece(stage, c, W + w)),
+                       reinterpret_cast<const uint8_t*>(a.dh_out) + at * (2 * W) + 16 * w);
+        }
+        if (a.b) cp_async16(smem_addr(piece(stage, c, 2 * W + 1)), reinterpret_cast<const uint8_t*>(a.b) + at * 2);
+      }
+    }
+    cp_async_commit();  // a group per row, empty past the last one
+  };
+
   float acc[3][CH][8];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -326,160 +439,182 @@ __global__ void __launch_bounds__(1024) k_block_norm_backward(const BackArgs a) 
       for (int i = 0; i < 8; ++i) acc[k][c][i] = 0.f;
     }
   }
-  int buf = 0;
-  for (int64_t row = first; row < last; ++row, buf ^= 1) {
-    const int64_t at = row * a.D;
-    float (*slot)[kMaxWarps] = slots[buf];
-    float x[CH][8], g[CH][8], u[CH][8], d[CH][8];
-    bool live[CH];
+  // Pieces of absent inputs and of columns past D read as zero.
+  for (int st = 0; st < a.stages; ++st) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * T + (int)threadIdx.x) * 8;
-      live[c] = col < a.D;
-      Raw8<FP32> rx, rd;
-      uint4 rn = make_uint4(0, 0, 0, 0), rb = make_uint4(0, 0, 0, 0);
-      rx.zero();
-      rd.zero();
-      if (live[c]) {
-        if (a.dn) {
-          rx.load(a.h, at + col);
-          rn = ld_stream(reinterpret_cast<const uint16_t*>(a.dn) + at + col);
-        }
-        if (a.dh_out) rd.load(a.dh_out, at + col);
-        if (a.b) rb = ld_stream(reinterpret_cast<const uint16_t*>(a.b) + at + col);
-      }
-      rx.get(x[c]);
-      rd.get(d[c]);
-      unpack8(rn, g[c]);
-      unpack8(rb, u[c]);
-    }
-    // Layer norms: the means first, so that the squares are those of centred
-    // values (a mean far above the deviation would cancel in FP32).
-    if (a.pre == kLayer || a.post == kLayer) {
-      float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          m[0] += x[c][i];
-          m[1] += u[c][i];
-        }
-      }
-      row_sums<2>(m, warps, slot);
-      const float mx = a.pre == kLayer ? m[0] * inv_d : 0.f;
-      const float mu = a.post == kLayer ? m[1] * inv_d : 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[c][i] = live[c] ? x[c][i] - mx : 0.f;
-          u[c][i] = live[c] ? u[c][i] - mu : 0.f;
-        }
-      }
-    }
-    // Squares of both rows, and the sums of g and g x with g = dn (1 + scale).
-    float q[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (!live[c]) continue;
-      const int col = (c * T + (int)threadIdx.x) * 8;
-      float sc[8];
-      load_mod8(a.scale, s * a.D + col, 0.f, sc);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[2][c][i] += g[c][i];
-        const float w = g[c][i] * (1.0f + sc[i]);
-        q[0] = fmaf(x[c][i], x[c][i], q[0]);
-        q[1] = fmaf(u[c][i], u[c][i], q[1]);
-        q[2] = fmaf(w, x[c][i], q[2]);
-        q[3] += w;
-      }
-    }
-    row_sums<4>(q, warps, slot + 2);
-    const float rx = 1.0f / sqrtf(q[0] * inv_d + a.eps);
-    const float ru = a.post == kNone ? 1.0f : 1.0f / sqrtf(q[1] * inv_d + a.eps);
-    const float mgx = q[2] * inv_d * rx;  // mean of g x^
-    const float mg = a.pre == kLayer ? q[3] * inv_d : 0.f;
-    float p[2] = {0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (!live[c]) continue;
-      const int col = (c * T + (int)threadIdx.x) * 8;
-      float sc[8], gt[8];
-      load_mod8(a.scale, s * a.D + col, 0.f, sc);
-      load_mod8(a.gate, s * a.D + col, 1.f, gt);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = x[c][i] * rx;
-        acc[1][c][i] = fmaf(g[c][i], xh, acc[1][c][i]);
-        if (a.dn) d[c][i] = fmaf(rx, g[c][i] * (1.0f + sc[i]) - mg - xh * mgx, d[c][i]);
-        u[c][i] *= ru;
-        acc[0][c][i] = fmaf(d[c][i], u[c][i], acc[0][c][i]);
-        const float w = gt[i] * d[c][i];
-        p[0] = fmaf(w, u[c][i], p[0]);
-        p[1] += w;
-        x[c][i] = w;
-      }
-    }
-    if (a.dh) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (!live[c]) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] *= a.alpha;
-        store_stream8<FP32>(a.dh, at + (c * T + (int)threadIdx.x) * 8, d[c]);
-      }
-    }
-    if (a.db) {
-      float mwu = 0.f, mw = 0.f;
-      if (a.post != kNone) {
-        row_sums<2>(p, warps, slot + 6);
-        mwu = p[0] * inv_d;
-        mw = a.post == kLayer ? p[1] * inv_d : 0.f;
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (!live[c]) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[c][i] = ru * (x[c][i] - mw - u[c][i] * mwu);
-        st_stream(reinterpret_cast<uint16_t*>(a.db) + at + (c * T + (int)threadIdx.x) * 8, pack8(x[c]));
-      }
+      for (int k = 0; k < PIECES; ++k) *piece(st, c, k) = make_uint4(0, 0, 0, 0);
     }
   }
-  float* out = a.sums + (int64_t)blockIdx.x * 3 * a.D;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int st = 0; st < a.stages; ++st) fetch(first + st, st);
+
+  int buf = 0, stage = 0;
+  for (int64_t row = first; row < last; ++row, buf ^= 1) {
+    cp_async_wait(a.stages - 1);
+    Raw8<FP32> rx8[CH], rd8[CH];
+    uint4 rn8[CH], rb8[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * T + (int)threadIdx.x) * 8;
-      if (col >= a.D) continue;
-      float4* o = reinterpret_cast<float4*>(out + (int64_t)k * a.D + col);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        rx8[c].q[w] = *piece(stage, c, w);
+        rd8[c].q[w] = *piece(stage, c, W + w);
+      }
+      rn8[c] = *piece(stage, c, 2 * W);
+      rb8[c] = *piece(stage, c, 2 * W + 1);
+    }
+    fetch(row + a.stages, stage);
+    if (++stage == a.stages) stage = 0;
+
+    float mx = 0.f, mu = 0.f;
+    if constexpr (LAYER) {
+      float m[8] = {};
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float x[8], u[8];
+        rx8[c].get(x);
+        unpack8(rb8[c], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          m[0] += x[i];
+          m[1] += u[i];
+        }
+      }
+      cta_sums<8>(m, warps, mean_slots[buf]);
+      if (a.pre == kLayer) mx = m[0] * inv_d;
+      if (a.post == kLayer) mu = m[1] * inv_d;
+    }
+    float q[N] = {};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (!live[c]) continue;
+      const int col = (c * T + t) * 8;
+      float x[8], d[8], g[8], u[8], sc[8], gt[8];
+      rx8[c].get(x);
+      rd8[c].get(d);
+      unpack8(rn8[c], g);
+      unpack8(rb8[c], u);
+      load_mod8(scale, col, 0.f, sc);
+      load_mod8(gate, col, 1.f, gt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[2][c][i] += g[i];
+        const float w = g[i] * (1.0f + sc[i]);
+        x[i] -= mx;
+        u[i] -= mu;
+        const float tb = gt[i] * u[i];
+        q[0] = fmaf(x[i], x[i], q[0]);
+        q[1] = fmaf(u[i], u[i], q[1]);
+        q[2] = fmaf(w, x[i], q[2]);
+        q[3] = fmaf(tb, d[i], q[3]);
+        q[4] = fmaf(tb, w, q[4]);
+        q[5] = fmaf(tb, x[i], q[5]);
+        if constexpr (LAYER) {
+          q[6] += w;
+          q[7] += tb;
+          q[8] = fmaf(gt[i], d[i], q[8]);
+          q[9] = fmaf(gt[i], w, q[9]);
+          q[10] += gt[i];
+          q[11] = fmaf(gt[i], x[i], q[11]);
+        }
+      }
+    }
+    cta_sums<N>(q, warps, slots[buf]);
+    const float rx = a.dn ? 1.0f / sqrtf(q[0] * inv_d + a.eps) : 0.f;
+    const float ru = a.post == kNone ? 1.0f : 1.0f / sqrtf(q[1] * inv_d + a.eps);
+    const float k = rx * rx * rx * (q[2] * inv_d);
+    float mg = 0.f, mw = 0.f, swu = q[3] + rx * q[4] - k * q[5];
+    if constexpr (LAYER) {
+      if (a.pre == kLayer) mg = q[6] * inv_d;
+      swu -= rx * mg * q[7];
+      if (a.post == kLayer) mw = inv_d * (q[8] + rx * (q[9] - mg * q[10]) - k * q[11]);
+    }
+    const float mwu = a.post == kNone ? 0.f : ru * swu * inv_d;  // mean of w u
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (!live[c]) continue;
+      const int col = (c * T + t) * 8;
+      float x[8], d[8], g[8], u[8], sc[8], gt[8];
+      rx8[c].get(x);
+      rd8[c].get(d);
+      unpack8(rn8[c], g);
+      unpack8(rb8[c], u);
+      load_mod8(scale, col, 0.f, sc);
+      load_mod8(gate, col, 1.f, gt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] -= mx;
+        u[i] = (u[i] - mu) * ru;
+        acc[1][c][i] = fmaf(g[i], x[i] * rx, acc[1][c][i]);
+        d[i] = fmaf(rx, g[i] * (1.0f + sc[i]) - mg, d[i]) - k * x[i];
+        acc[0][c][i] = fmaf(d[i], u[i], acc[0][c][i]);
+        u[i] = ru * (gt[i] * d[i] - mw - u[i] * mwu);
+        d[i] *= a.alpha;
+      }
+      const int64_t at = row * a.D + col;
+      if (a.dh) store_stream8<FP32>(a.dh, at, d);
+      if (a.db) st_stream(reinterpret_cast<uint16_t*>(a.db) + at, pack8(u));
+    }
+  }
+  cp_async_wait(0);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (!a.sums[k]) continue;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (!live[c]) continue;
+      float4* o = reinterpret_cast<float4*>(a.sums[k] + blockIdx.x * a.sum_stride + (c * T + t) * 8);
       o[0] = make_float4(acc[k][c][0], acc[k][c][1], acc[k][c][2], acc[k][c][3]);
       o[1] = make_float4(acc[k][c][4], acc[k][c][5], acc[k][c][6], acc[k][c][7]);
     }
   }
 }
 
-// out_k[s] = the sum of a segment's partials, in the order of its chunks.
-__global__ void __launch_bounds__(128) k_segment_sums(const float* __restrict__ sums, int64_t seg_chunks, int D,
-                                                      float* __restrict__ o0, float* __restrict__ o1,
-                                                      float* __restrict__ o2, int64_t S) {
-  const int col = (blockIdx.x * 128 + threadIdx.x) * 4;
-  if (col >= D) return;
-  float* out = blockIdx.z == 0 ? o0 : (blockIdx.z == 1 ? o1 : o2);
+struct SumArgs {
+  const float* sums;  // [chunks][3][D]
+  float* out[3];
+  int64_t seg_chunks, segments, chunks;
+  int D;
+};
+
+// out_k[s] = the sum of a segment's partials: eight warps take every eighth
+// chunk of 128 columns, then add up in the order of the warps.
+__global__ void __launch_bounds__(256) k_segment_sums(const SumArgs a) {
+  __shared__ float4 part[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = ((int)blockIdx.x * 32 + lane) * 4;
+  float* out = a.out[blockIdx.z];
   if (!out) return;
-  for (int64_t s = blockIdx.y; s < S; s += gridDim.y) {
-    const float* src = sums + (s * seg_chunks * 3 + blockIdx.z) * D + col;
+  for (int64_t s = blockIdx.y; s < a.segments; s += gridDim.y) {
+    const int64_t c0 = s * a.seg_chunks;
+    const int64_t c1 = s + 1 < a.segments ? c0 + a.seg_chunks : a.chunks;
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < a.D) {
+      const float* src = a.sums + blockIdx.z * a.D + col;
 #pragma unroll 8
-    for (int64_t i = 0; i < seg_chunks; ++i) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(src + i * 3 * D));
-      t.x += v.x;
-      t.y += v.y;
-      t.z += v.z;
-      t.w += v.w;
+      for (int64_t i = c0 + warp; i < c1; i += 8) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(src + i * 3 * a.D));
+        t.x += v.x;
+        t.y += v.y;
+        t.z += v.z;
+        t.w += v.w;
+      }
     }
-    *reinterpret_cast<float4*>(out + s * D + col) = t;
+    part[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && col < a.D) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) {
+        const float4 v = part[w][lane];
+        t.x += v.x;
+        t.y += v.y;
+        t.z += v.z;
+        t.w += v.w;
+      }
+      *reinterpret_cast<float4*>(out + s * a.D + col) = t;
+    }
+    __syncthreads();
   }
 }
 
@@ -501,8 +636,37 @@ cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);
 }
 
-// Rows per CTA of the backward pass.
-constexpr int64_t kChunkRows = 64;
+// Threads of a backward CTA: eight columns each up to D = 7168, sixteen above.
+int back_threads(int D) { return D <= 7168 ? 32 * ((D / 8 + 31) / 32) : 32 * ((D / 8 + 63) / 64); }
+
+// How the backward pass splits its rows: `per` chunks of `rows` rows in a full
+// segment, `total` in all.  A chunk stays within a segment.
+struct Chunks {
+  int64_t segments, rows, per, total;
+};
+Chunks back_chunks(int64_t M, int D, int64_t seg) {
+  if (seg > M) seg = M;
+  Chunks c;
+  c.segments = (M + seg - 1) / seg;
+  const int64_t rest = M - (c.segments - 1) * seg;
+  // One wave: the CTAs that 148 SMs hold at ~72 registers a thread.  A CTA's
+  // partial sums cost as much traffic as about one of its rows, and its
+  // rows follow one another: not less than four of them.
+  const int64_t resident = 896 / back_threads(D) < 1 ? 1 : 896 / back_threads(D);
+  const int64_t target = 148 * (resident > 8 ? 8 : resident);
+  c.rows = (M + target - 1) / target;
+  if (c.rows < 4) c.rows = 4;
+  if (c.rows > seg) c.rows = seg;
+  for (;;) {
+    c.per = (seg + c.rows - 1) / c.rows;
+    c.total = (c.segments - 1) * c.per + (rest + c.rows - 1) / c.rows;
+    // Segments' ragged ends may open a second wave: take longer chunks.
+    if (c.total <= target || c.rows >= seg || c.segments >= target) break;
+    c.rows += (c.rows + 31) / 32;
+    if (c.rows > seg) c.rows = seg;
+  }
+  return c;
+}
 
 }  // namespace
 
@@ -529,14 +693,46 @@ cudaError_t launch_block_norm(const BlockNormLaunch& p, cudaStream_t s) {
   return p.fp32 ? norm_dispatch<true>(a, s) : norm_dispatch<false>(a, s);
 }
 
-int64_t block_norm_backward_chunks(int64_t M, int64_t segment_tokens, int64_t* per_segment) {
-  const int64_t S = (M + segment_tokens - 1) / segment_tokens;
-  const int64_t rows = segment_tokens < M ? segment_tokens : M;
-  *per_segment = (rows + kChunkRows - 1) / kChunkRows;
-  return S * *per_segment;
+size_t block_norm_backward_workspace(int64_t M, int D, int64_t segment_tokens) {
+  const Chunks c = back_chunks(M, D, segment_tokens);
+  return c.per == 1 ? 0 : (size_t)c.total * 3 * D * sizeof(float);  // one chunk per segment: nothing to add up
 }
 
+namespace {
+
+template <bool FP32, int CH, bool LAYER>
+cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
+  const size_t stage = (size_t)CH * (FP32 ? 6 : 4) * 16 * T;
+  int stages = (int)(kBackSmem / stage);
+  if (stages > kBackStagesMax) stages = kBackStagesMax;
+  if (stages < 1) stages = 1;  // the widest FP32 rows: 192 KB, which still fits
+  if (stages > a.chunk_rows) stages = (int)a.chunk_rows;
+  a.stages = stages;
+  const size_t smem = stage * stages;
+  // A kernel asks for more than 48 KB first.  Always the same amount: calls
+  // from several host threads cannot lower each other's; a context keeps it,
+  // and asking again costs well under a launch.
+  const cudaError_t e = cudaFuncSetAttribute((const void*)k_block_norm_backward<FP32, CH, LAYER>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBackSmem);
+  if (e != cudaSuccess) return e;
+  k_block_norm_backward<FP32, CH, LAYER><<<(unsigned)chunks, T, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool FP32>
+cudaError_t back_dispatch(BackArgs& a, int64_t chunks, cudaStream_t s) {
+  const int T = back_threads(a.D);
+  const bool layer = a.pre == kLayer || a.post == kLayer;
+  if (a.D <= 7168) {
+    return layer ? back_launch<FP32, 1, true>(a, chunks, T, s) : back_launch<FP32, 1, false>(a, chunks, T, s);
+  }
+  return layer ? back_launch<FP32, 2, true>(a, chunks, T, s) : back_launch<FP32, 2, false>(a, chunks, T, s);
+}
+
+}  // namespace
+
 cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* kernels, cudaStream_t s) {
+  const Chunks c = back_chunks(p.M, p.D, p.segment_tokens);
   BackArgs a;
   a.dn = p.dn;
   a.dh_out = p.dh_out;
@@ -546,36 +742,34 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* ke
   a.scale = p.scale;
   a.dh = p.dh;
   a.db = p.db;
-  a.sums = p.workspace;
   a.M = p.M;
   a.seg = p.segment_tokens < p.M ? p.segment_tokens : p.M;
-  const int64_t chunks = block_norm_backward_chunks(p.M, a.seg, &a.seg_chunks);
-  a.chunk_rows = kChunkRows;
+  a.seg_chunks = c.per;
+  a.segments = c.segments;
+  a.chunk_rows = c.rows;
   a.D = p.D;
   a.post = p.post;
   a.pre = p.pre;
   a.alpha = p.alpha;
   a.eps = p.eps;
-  const int T = 32 * ((p.D / 8 + 31) / 32);
+  float* const out[3] = {p.dgate, p.dscale, p.dshift};
+  const bool direct = c.per == 1;
+  for (int k = 0; k < 3; ++k) a.sums[k] = !out[k] ? nullptr : (direct ? out[k] : p.workspace + (int64_t)k * p.D);
+  a.sum_stride = direct ? p.D : 3 * (int64_t)p.D;
   *kernels = 1;
-  if (p.D <= 8192) {
-    if (p.fp32) k_block_norm_backward<true, 1><<<(unsigned)chunks, T, 0, s>>>(a);
-    else k_block_norm_backward<false, 1><<<(unsigned)chunks, T, 0, s>>>(a);
-  } else {
-    const int T2 = 32 * ((p.D / 8 + 63) / 64);
-    if (p.fp32) k_block_norm_backward<true, 2><<<(unsigned)chunks, T2, 0, s>>>(a);
-    else k_block_norm_backward<false, 2><<<(unsigned)chunks, T2, 0, s>>>(a);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (p.dgate || p.dscale || p.dshift) {
-    const int64_t S = chunks / a.seg_chunks;
-    const dim3 grid((unsigned)((p.D / 4 + 127) / 128), (unsigned)(S < 65535 ? S : 65535), 3);
-    k_segment_sums<<<grid, 128, 0, s>>>(a.sums, a.seg_chunks, p.D, p.dgate, p.dscale, p.dshift, S);
-    *kernels = 2;
-    e = cudaGetLastError();
-  }
-  return e;
+  cudaError_t e = p.fp32 ? back_dispatch<true>(a, c.total, s) : back_dispatch<false>(a, c.total, s);
+  if (e != cudaSuccess || direct || (!out[0] && !out[1] && !out[2])) return e;
+  SumArgs m;
+  m.sums = p.workspace;
+  for (int k = 0; k < 3; ++k) m.out[k] = out[k];
+  m.seg_chunks = c.per;
+  m.segments = c.segments;
+  m.chunks = c.total;
+  m.D = p.D;
+  const dim3 grid((unsigned)((p.D + 127) / 128), (unsigned)(c.segments < 65535 ? c.segments : 65535), 3);
+  k_segment_sums<<<grid, 256, 0, s>>>(m);
+  *kernels = 2;
+  return cudaGetLastError();
 }
 
 }  // namespace lg

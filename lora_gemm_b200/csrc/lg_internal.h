@@ -91,9 +91,8 @@ struct BlockNormBackwardLaunch {
   int post, pre;
   float alpha, eps;
 };
-// Chunks of rows the backward pass works in (each holds 3 D partial sums in
-// the workspace), and how many a full segment has.
-int64_t block_norm_backward_chunks(int64_t M, int64_t segment_tokens, int64_t* per_segment);
+// Bytes of partial column sums (0: none are needed); M >= 1.
+size_t block_norm_backward_workspace(int64_t M, int D, int64_t segment_tokens);
 // *kernels: launches made.
 cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* kernels, cudaStream_t s);
 

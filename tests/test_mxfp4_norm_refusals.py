@@ -92,7 +92,7 @@ def test_block_norm_refusals():
 
 def _back(work=at(20), nbytes=1 << 40, **kw):
     f = dict(dn=at(0), dh_out=at(1), h_out=at(2), b=at(3), gate=at(4), scale=at(5), dh=at(6), db=at(7), dgate=at(8),
-             dscale=at(9), dshift=at(10), M=10, segment_tokens=4, D=256, stream_type=1, post=1, pre=1, alpha=1.0,
+             dscale=at(9), dshift=at(10), M=100, segment_tokens=50, D=256, stream_type=1, post=1, pre=1, alpha=1.0,
              eps=1e-6)
     f.update(kw)
     return L.lg_block_norm_backward(ctypes.byref(lg.BlockNormBackwardArgs(**f)), work, nbytes, None)
@@ -113,9 +113,10 @@ def test_block_norm_backward_refusals():
         for arg in ("dn", "dh_out", "h_out", "b", "gate", "scale") + outs[:i]:
             if (out, arg) != ("dh", "dh_out"):
                 assert _back(**{out: at(21), arg: at(21)}) == INVALID, (out, arg)
-    need = lg.block_norm_backward_workspace_size(10, 256, 4)
-    if need:
-        assert _back(nbytes=need - 1) == WORKSPACE and _back(work=None) == WORKSPACE
+    need = lg.block_norm_backward_workspace_size(100, 256, 50)
+    assert need > 0 and _back(nbytes=need - 1) == WORKSPACE and _back(work=None) == WORKSPACE
+    # Segments of a chunk or less have no partial sums: no workspace.
+    assert lg.block_norm_backward_workspace_size(100, 256, 1) == 0
     assert _back(M=0) == lg.LG_OK and _back(M=0, dh=at(1)) == lg.LG_OK
     for bad in ((0, 256, 4), (10, 12, 4), (10, 256, 0), (10, 1 << 20, 4)):
         assert lg.block_norm_backward_workspace_size(*bad) == 0
