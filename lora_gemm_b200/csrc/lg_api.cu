@@ -461,7 +461,9 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   cudaStream_t s = as_stream(stream);
   uint16_t* wsA = nullptr;
   uint16_t* wsB = nullptr;
-  if (R > 0) {
+  // Few tokens read the FP32 factors where they are.
+  const bool few = mx && mx->bits == 4 && lg::few_tokens(M);
+  if (R > 0 && !few) {
     wsA = reinterpret_cast<uint16_t*>(workspace);
     wsB = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + align256(2ull * R * K));
     st = launched(lg::launch_prep_bf16(A_cat, B_cat, wsA, wsB, (int64_t)R * K, (int64_t)N * R, sms, s), 1);
@@ -498,6 +500,12 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
     p.ffn = N / 2;
     p.q_codes = sw->codes;
     p.q_scales = sw->scales;
+  }
+  if (few) {
+    int kernels = 0;
+    const cudaError_t e = lg::launch_lora_linear_few(p, A_cat, B_cat, reinterpret_cast<uint16_t*>(workspace), &kernels, s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return launched(e, (uint64_t)kernels);
   }
   bool driver_failed = false;
   cudaError_t e = lg::launch_lora_linear(p, s, &driver_failed);
@@ -556,6 +564,8 @@ lg_status lg_lora_linear_mxfp8(const void* x, const void* x_codes, const void* x
 }
 
 size_t lg_lora_linear_mxfp4_workspace_size(int64_t M, int K, int N, int R) {
+  // The bf16 factors; h of a few-token call (M * R values, M <= 64) is smaller
+  // than A_cat's copy (K * R, K >= 128).
   if (K % 128) return 0;
   return lg_lora_linear_workspace_size(M, K, N, R);
 }

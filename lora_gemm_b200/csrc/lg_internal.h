@@ -132,6 +132,12 @@ struct LinearLaunch {
 // the tensor-map encoder (driver API) is missing or rejects a map.
 cudaError_t launch_lora_linear(const LinearLaunch& p, cudaStream_t s, bool* driver_failed);
 
+// lg_lora_linear_mxfp4 for few tokens: FP32 factors as they are, h a workspace
+// of M * R bf16 values.  *kernels: launches made.
+bool few_tokens(int64_t M);
+cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, const float* B_cat, uint16_t* h,
+                                   int* kernels, cudaStream_t s);
+
 // CTAs per cluster sharing one panel in lg_lora_linear (0: chosen per shape).
 void set_cluster_override(int g);
 // MMA variant of lg_lora_linear: 1 single-SM, 2 SM pair (0: chosen per shape).
