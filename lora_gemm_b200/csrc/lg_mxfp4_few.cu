@@ -75,15 +75,17 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
-// Eight FP32 values -> four bf16 pairs, rounded to nearest (as the other
-// layers round the factors for the tensor cores).
+// FP32 values -> bf16 pairs, rounded to nearest (as the other layers round the
+// factors for the tensor cores).
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
 __device__ __forceinline__ void round8(const float4& a, const float4& b, uint32_t (&h)[4]) {
-  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    h[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
+  h[0] = round2(a.x, a.y);
+  h[1] = round2(a.z, a.w);
+  h[2] = round2(b.x, b.y);
+  h[3] = round2(b.z, b.w);
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -121,56 +123,150 @@ struct UpArgs {
   int M, K, N, R;
 };
 
+// NG: groups of eight tokens.
 template <int NG>
 struct UpCfg {
   static constexpr int kX = NG * 8 * 64;                                // x codes per stage
   static constexpr int kStage = kStageRows + kUpRows * 4 + kX + NG * 8 * 4;  // + W scale words, x scale words
-  static constexpr int kStages = NG >= 8 ? 3 : 4;
+  // Two CTAs per SM (227 KB shared, 128 registers a thread) keep 16 warps and
+  // over 80 KB of copies in flight.
+  static constexpr int kStages = NG == 1 ? 4 : (NG <= 4 ? 3 : 2);
   static constexpr int kWarp = kStage * kStages;
   static constexpr int kSums = kUpWarps * kUpRows * NG * 8 * 4;
   static constexpr int kSmem = kUpWarps * kWarp > kSums ? kUpWarps * kWarp : kSums;
 };
 
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+// (c, c1) += (d, d1) * s, two FP32 lanes in one instruction.
+__device__ __forceinline__ void fma2(float& c, float& c1, float d, float d1, uint64_t s) {
+  uint64_t v = pair2(c, c1);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(pair2(d, d1)), "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(c), "=f"(c1) : "l"(v));
+}
+
+// One stage of 128 K: acc += deq(W) deq(x)^T.  PLAIN: every scale's exponent
+// field is in [63, 190] (plain_scales), so a scale is its byte in FP32's
+// exponent field and the product of two is exact.
+template <int NG, bool PLAIN>
+__device__ __forceinline__ void up_stage(uint32_t st, uint32_t xc, int g, int t, const uint32_t (&ws)[4],
+                                         const uint32_t (&xs)[NG][2], float (&acc)[2][NG][4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {  // the four blocks of 32
+    uint32_t w[4][4];
+    float sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + g;
+      decode8(lds32(st + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), w[i]);
+      sw[i] = PLAIN ? __uint_as_float((c == 3 ? ws[i] >> 1 : ws[i] << (23 - 8 * c)) & 0x7F800000u)
+                    : e8m0((ws[i] >> (8 * c)) & 255u);
+    }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      uint32_t x[4];
+      const int r = n * 8 + g;
+      decode8(lds32(xc + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), x);
+      float sx[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sx[e] = PLAIN ? __uint_as_float((c == 3 ? xs[n][e] >> 1 : xs[n][e] << (23 - 8 * c)) & 0x7F800000u)
+                      : e8m0((xs[n][e] >> (8 * c)) & 255u);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(d, w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x[0], x[1]);
+        mma_f16(d, w[2 * i][2], w[2 * i + 1][2], w[2 * i][3], w[2 * i + 1][3], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float(&o)[4] = acc[i][n];
+          const float s = sw[2 * i + e];
+          if (PLAIN) {
+            fma2(o[2 * e], o[2 * e + 1], d[2 * e], d[2 * e + 1], mul2(pair2(sx[0], sx[1]), pair2(s, s)));
+          } else {
+            // The smaller scale first: no step leaves FP32's range unless the
+            // result does.  (fminf drops a NaN, the sum s + sx keeps it.)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float lo = fminf(s, sx[k]), hi = s + sx[k] == s + sx[k] ? fmaxf(s, sx[k]) : s + sx[k];
+              o[2 * e + k] += (d[2 * e + k] * lo) * hi;
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int NG>
-__global__ void __launch_bounds__(kUpWarps * 32) k_few_up(const UpArgs a) {
+__global__ void __launch_bounds__(kUpWarps * 32, 2) k_few_up(const UpArgs a) {
   using C = UpCfg<NG>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kUpRows;
-  const int groups = a.K / 128;  // of 128 K: warp w takes w, w + 8, ...
+  // The steps of this CTA: groups of 128 K, then 16 ranks of the adapters'
+  // term each.  Warp w takes steps w, w + 8, ...
+  const int groups = a.K / 128;
+  const int steps = groups + a.R / 16;
   const int64_t row_bytes = a.K / 2;
   const uint32_t ring = s_addr(smem) + warp * C::kWarp;
+  bool waited = false;
 
-  // Stage layout: W codes [32 rows][64 B], 16-byte piece c of row r at
-  // c ^ ((r / 2) mod 4) (no bank conflicts when eight rows are read at one
-  // piece); W scale words [32]; x codes [NG * 8][64 B] likewise; x scale words.
+  // Stage layout: W codes [32 rows][64 B] (or 16 FP32 ranks of B_cat), 16-byte
+  // piece c of row r at c ^ ((r / 2) mod 4): no bank conflicts when eight rows
+  // are read at one piece; W scale words [32]; x codes [NG * 8][64 B] (or 32 B
+  // of h) likewise; x scale words.
   constexpr uint32_t kWs = kStageRows, kXc = kWs + kUpRows * 4, kXs = kXc + C::kX;
-  auto fetch = [&](int kg, int stage) {
+  auto fetch = [&](int step, int stage) {
     const uint32_t st = ring + stage * C::kStage;
-    if (kg < groups) {
+    if (step < groups) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + g;
-        copy16(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.wq + (n0 + r) * row_bytes + kg * 64 + t * 16);
+        copy16(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.wq + (n0 + r) * row_bytes + step * 64 + t * 16);
       }
       // Row r of a group of 128 has its four scale bytes at 16 (r mod 32) + 4 (r / 32).
       copy4(st + kWs + lane * 4,
-            a.wsf + (((int64_t)(n0 >> 7) * groups + kg) << 9) + 16 * lane + 4 * ((n0 & 127) >> 5));
+            a.wsf + (((int64_t)(n0 >> 7) * groups + step) << 9) + 16 * lane + 4 * ((n0 & 127) >> 5));
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const int r = n * 8 + g;
-        if (r < a.M) copy16(st + kXc + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.xq + r * row_bytes + kg * 64 + t * 16);
+        if (r < a.M) copy16(st + kXc + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.xq + r * row_bytes + step * 64 + t * 16);
       }
 #pragma unroll
       for (int n = 0; n < (NG + 3) / 4; ++n) {
         const int r = n * 32 + lane;
-        if (r < a.M && r < NG * 8) copy4(st + kXs + r * 4, a.xsf + ((int64_t)kg << 9) + 16 * lane + 4 * n);
+        if (r < a.M && r < NG * 8) copy4(st + kXs + r * 4, a.xsf + ((int64_t)step << 9) + 16 * lane + 4 * n);
+      }
+    } else if (step < steps) {
+      const int r0 = (step - groups) * 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + g;
+        copy16(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.B + (int64_t)(n0 + r) * a.R + r0 + t * 4);
+      }
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is there
+      waited = true;
+#pragma unroll
+      for (int n = 0; n < (NG + 1) / 2; ++n) {
+        const int r = n * 16 + (lane >> 1), c = lane & 1;
+        if (r < a.M && r < NG * 8)
+          copy16(st + kXc + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), a.h + (int64_t)r * a.R + r0 + c * 8);
       }
     }
     copy_commit();
   };
-  // Tokens past M: codes 0 under scale 1, never overwritten.
+  // Tokens past M: codes (or h) 0 under scale 1, never overwritten.
   for (int st = 0; st < C::kStages; ++st) {
     uint8_t* base = smem + warp * C::kWarp + st * C::kStage;
     for (int i = lane; i < C::kX / 16; i += 32) reinterpret_cast<uint4*>(base + kXc)[i] = make_uint4(0, 0, 0, 0);
@@ -190,99 +286,60 @@ __global__ void __launch_bounds__(kUpWarps * 32) k_few_up(const UpArgs a) {
     }
   }
   int stage = 0;
-  for (int kg = warp; kg < groups; kg += kUpWarps) {
+  for (int step = warp; step < steps; step += kUpWarps) {
     copy_wait<C::kStages - 1>();
     __syncwarp();  // every lane's pieces of this stage have landed
     const uint32_t st = ring + stage * C::kStage;
-    uint32_t ws[4];  // scale words of rows g, g + 8, g + 16, g + 24
+    if (step < groups) {
+      uint32_t ws[4];  // scale words of rows g, g + 8, g + 16, g + 24
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ws[i] = lds32(st + kWs + (i * 8 + g) * 4);
-    uint32_t xs[NG][2];  // of tokens 8 n + 2 t and + 1
-    bool plain = plain_scales(ws[0]) && plain_scales(ws[1]) && plain_scales(ws[2]) && plain_scales(ws[3]);
+      for (int i = 0; i < 4; ++i) ws[i] = lds32(st + kWs + (i * 8 + g) * 4);
+      uint32_t xs[NG][2];  // of tokens 8 n + 2 t and + 1
+      bool plain = plain_scales(ws[0]) && plain_scales(ws[1]) && plain_scales(ws[2]) && plain_scales(ws[3]);
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      xs[n][0] = lds32(st + kXs + (n * 8 + 2 * t) * 4);
-      xs[n][1] = lds32(st + kXs + (n * 8 + 2 * t + 1) * 4);
-      plain = plain && plain_scales(xs[n][0]) && plain_scales(xs[n][1]);
-    }
-    plain = __all_sync(0xffffffffu, plain);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {  // the four blocks of 32
-      uint32_t w[4][4];
-      float sw[4];
+      for (int n = 0; n < NG; ++n) {
+        xs[n][0] = lds32(st + kXs + (n * 8 + 2 * t) * 4);
+        xs[n][1] = lds32(st + kXs + (n * 8 + 2 * t + 1) * 4);
+        plain = plain && plain_scales(xs[n][0]) && plain_scales(xs[n][1]);
+      }
+      if (__all_sync(0xffffffffu, plain)) {
+        up_stage<NG, true>(st, st + kXc, g, t, ws, xs, acc);
+      } else {
+        up_stage<NG, false>(st, st + kXc, g, t, ws, xs, acc);
+      }
+    } else {
+      // 16 ranks: lane t has ranks 4 t .. 4 t + 3 of its rows and tokens.
+      uint32_t w[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + g;
-        decode8(lds32(st + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), w[i]);
-        sw[i] = e8m0((ws[i] >> (8 * c)) & 255u);
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4))
+                     : "memory");
+        w[i][0] = round2(v.x, v.y);
+        w[i][1] = round2(v.z, v.w);
       }
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        uint32_t x[4];
         const int r = n * 8 + g;
-        decode8(lds32(st + kXc + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), x);
-        const float sx[2] = {e8m0((xs[n][0] >> (8 * c)) & 255u), e8m0((xs[n][1] >> (8 * c)) & 255u)};
+        uint32_t x0, x1;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(x0), "=r"(x1)
+                     : "r"(st + kXc + r * 64 + (((t >> 1) ^ ((r >> 1) & 3)) << 4) + (t & 1) * 8)
+                     : "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(d, w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x[0], x[1]);
-          mma_f16(d, w[2 * i][2], w[2 * i + 1][2], w[2 * i][3], w[2 * i + 1][3], x[2], x[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s0 = sw[2 * i + (e >> 1)], s1 = sx[e & 1];
-            if (plain) {
-              acc[i][n][e] = fmaf(d[e], s0 * s1, acc[i][n][e]);
-            } else {
-              // The smaller scale first: no step leaves FP32's range unless
-              // the result does.  (fminf drops a NaN, the sum s0 + s1 keeps it.)
-              const float lo = fminf(s0, s1), hi = s0 + s1 == s0 + s1 ? fmaxf(s0, s1) : s0 + s1;
-              acc[i][n][e] += (d[e] * lo) * hi;
-            }
-          }
-        }
+        for (int i = 0; i < 2; ++i) mma_bf16(acc[i][n], w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x0, x1);
       }
     }
     __syncwarp();  // the stage has been read by every lane
-    fetch(kg + C::kStages * kUpWarps, stage);
+    fetch(step + C::kStages * kUpWarps, stage);
     if (++stage == C::kStages) stage = 0;
   }
   copy_wait<0>();
-
-  // The adapters' term: 32 ranks a step, lane t has ranks 8 t .. 8 t + 7.
-  if (a.R > 0) {
-    bool waited = false;
-    for (int s = warp; s < a.R / 32; s += kUpWarps) {
-      float4 lo[4], hi[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* p = a.B + (int64_t)(n0 + i * 8 + g) * a.R + s * 32 + t * 8;
-        lo[i] = ld_stream4(p);
-        hi[i] = ld_stream4(p + 4);
-      }
-      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is there
-      waited = true;
-      uint32_t w[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) round8(lo[i], hi[i], w[i]);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (n * 8 + g < a.M) {
-          asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                       : "l"(a.h + (int64_t)(n * 8 + g) * a.R + s * 32 + t * 8)
-                       : "memory");
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma_bf16(acc[i][n], w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x.x, x.y);
-          mma_bf16(acc[i][n], w[2 * i][2], w[2 * i + 1][2], w[2 * i][3], w[2 * i + 1][3], x.z, x.w);
-        }
-      }
-    }
-    // Also where no step was this warp's: the grid ends after k_few_down.
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
+  // Also where no adapter step was this warp's: the grid ends after k_few_down.
+  if (a.R > 0 && !waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Join the warps' sums in their order: [warp][token][32 outputs].
   __syncthreads();  // every warp is done with its ring
@@ -427,7 +484,9 @@ cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, co
                                    int* kernels, cudaStream_t s) {
   if (p.M <= 8) return few_launch<1>(p, A_cat, B_cat, h, kernels, s);
   if (p.M <= 16) return few_launch<2>(p, A_cat, B_cat, h, kernels, s);
+  if (p.M <= 24) return few_launch<3>(p, A_cat, B_cat, h, kernels, s);
   if (p.M <= 32) return few_launch<4>(p, A_cat, B_cat, h, kernels, s);
+  if (p.M <= 48) return few_launch<6>(p, A_cat, B_cat, h, kernels, s);
   return few_launch<8>(p, A_cat, B_cat, h, kernels, s);
 }
 
