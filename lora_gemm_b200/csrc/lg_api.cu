@@ -411,7 +411,8 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   if (mx && (!aligned16(mx->xq) || !aligned16(mx->xsf) || !aligned16(mx->wq) || !aligned16(mx->wsf)))
     return LG_ERR_MISALIGNED;
   if (R > 0 && (!aligned16(A_cat) || !aligned16(B_cat))) return LG_ERR_MISALIGNED;
-  const size_t need = R > 0 && !check_only ? factor_copy_bytes(K, N, R) : 0;
+  const bool mx4 = mx && mx->bits == 4;
+  const size_t need = R > 0 && !check_only ? factor_copy_bytes(K, N, R) + (mx4 ? (size_t)align256(2ull * M * R) : 0) : 0;
   if (R > 0 && !check_only) {
     if (!workspace || ws_bytes < need) return LG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LG_ERR_MISALIGNED;
@@ -449,7 +450,7 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   if (R > 0 && (overlaps(workspace, need, A_cat, 4ull * R * K) || overlaps(workspace, need, B_cat, 4ull * N * R) ||
                 overlaps(workspace, need, x, bx) || (!mx && overlaps(workspace, need, W, bw))))
     return LG_ERR_INVALID_ARG;
-  if (R > 0 && mx && mx->bits == 4 &&
+  if (R > 0 && mx4 &&
       (overlaps(workspace, need, mx->xq, bxq) || overlaps(workspace, need, mx->wq, bwq) ||
        overlaps(workspace, need, mx->xsf, lg_mx_scale_bytes(M, K)) ||
        overlaps(workspace, need, mx->wsf, lg_mx_scale_bytes(N, K))))
@@ -462,7 +463,7 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   uint16_t* wsA = nullptr;
   uint16_t* wsB = nullptr;
   // Few tokens read the FP32 factors where they are.
-  const bool few = mx && mx->bits == 4 && lg::few_tokens(M);
+  const bool few = mx4 && lg::few_tokens(M);
   if (R > 0 && !few) {
     wsA = reinterpret_cast<uint16_t*>(workspace);
     wsB = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + align256(2ull * R * K));
@@ -504,6 +505,14 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   if (few) {
     int kernels = 0;
     const cudaError_t e = lg::launch_lora_linear_few(p, A_cat, B_cat, reinterpret_cast<uint16_t*>(workspace), &kernels, s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return launched(e, (uint64_t)kernels);
+  }
+  if (mx4) {
+    int kernels = 0;
+    bool failed = false;
+    uint16_t* h = R > 0 ? wsB + align256(2ull * N * R) / 2 : nullptr;
+    const cudaError_t e = lg::launch_lora_linear_tiles(p, h, &kernels, s, &failed);
     if (e != cudaSuccess) cudaGetLastError();
     return launched(e, (uint64_t)kernels);
   }
@@ -564,10 +573,9 @@ lg_status lg_lora_linear_mxfp8(const void* x, const void* x_codes, const void* x
 }
 
 size_t lg_lora_linear_mxfp4_workspace_size(int64_t M, int K, int N, int R) {
-  // The bf16 factors; h of a few-token call (M * R values, M <= 64) is smaller
-  // than A_cat's copy (K * R, K >= 128).
-  if (K % 128) return 0;
-  return lg_lora_linear_workspace_size(M, K, N, R);
+  // The bf16 factors and h [M, R] bf16 (few tokens: h alone, in their place).
+  const size_t factors = K % 128 ? 0 : lg_lora_linear_workspace_size(M, K, N, R);
+  return factors == 0 ? 0 : factors + (size_t)align256(2ull * M * R);
 }
 
 lg_status lg_lora_linear_mxfp4(const void* x, const void* x_codes, const void* x_scales, const void* W_codes,

@@ -146,6 +146,15 @@ void set_variant_override(int v);
 // Device error word of the current device: read and clear (synchronous on s).
 cudaError_t read_and_clear_device_error(cudaStream_t s, int* value);
 
+// The same for the tile kernel's own error word (no synchronization before).
+cudaError_t take_tile_error(int* value);
+
+// lg_lora_linear_mxfp4 on output tiles: h = x A^T into `h` (workspace, M * R
+// bf16) and y = deq(x) deq(W)^T + h B^T, the factors in bf16.  *kernels:
+// launches made.
+cudaError_t launch_lora_linear_tiles(const LinearLaunch& p, uint16_t* h, int* kernels, cudaStream_t s,
+                                     bool* driver_failed);
+
 // The driver's process-unique id of the calling thread's current CUDA
 // context.  False when no context is current or the driver cannot say; a
 // per-device cache keyed on this id notices a context that was destroyed

@@ -59,15 +59,13 @@
 #include "../../include/lora_gemm.h"
 #include "lg_device.cuh"
 #include "lg_internal.h"
+#include "lg_pipeline.cuh"
 
 namespace lg {
-
-__device__ int g_device_error;
 
 namespace {
 
 constexpr int BM = 128;      // token rows per CTA = TMEM lanes
-constexpr int BK = 64;       // K elements per stage: one 128-byte swizzle span
 constexpr int HC_MAX = 192;  // rank columns per down-projection chunk
 constexpr int RMAX = 576;
 constexpr uint32_t A_BYTES = BM * BK * 2;  // 16 KiB: this CTA's x tile
@@ -76,15 +74,12 @@ constexpr uint32_t ACC_COL = 0;
 constexpr int NUM_THREADS = 320;  // producer, MMA, 8 epilogue warps
 constexpr int EPI_WARPS = 8;      // two per TMEM lane quarter, one per half tile
 constexpr int MAX_STAGES = 8;
-constexpr uint64_t TEARDOWN_LIMIT_NS = 200ull * 1000ull * 1000ull;
 constexpr size_t kMaxSmem = 232448;  // sm_100 opt-in maximum per block
 
 constexpr uint32_t H_TILE_BYTES = BM * BK * 2;  // 16 KiB: 64 ranks of h for 128 rows
-constexpr int BKQ = 128;                        // K elements of a scale group (MXFP8: of a stage, 128-byte rows)
 constexpr uint32_t SF_GROUP_BYTES = 512;         // MXFP8 scales of 128 rows x 128 K
 // Pair variant: y leaves through a TMA store, staged per epilogue warp in
 // 32 x 32 bf16 boxes (64-byte rows, 64-byte swizzle).
-constexpr int Y_BOX = 32;
 constexpr uint32_t Y_WARP_BYTES = Y_BOX * Y_BOX * 2;              // 2 KiB
 constexpr uint32_t Y_STAGE_BYTES = 8 * Y_WARP_BYTES;              // 16 KiB for the 8 epilogue warps
 
@@ -223,61 +218,6 @@ struct Args {
   float eu_dt;
   unsigned long long wait_limit_ns;
 };
-
-__device__ __forceinline__ void record_timeout(volatile int* abort_flag) {
-  *abort_flag = 1;
-  atomicCAS(&g_device_error, 0, (int)LG_ERR_DEVICE_TIMEOUT);
-}
-
-// Wait for the phase of `bar` with parity `parity` to complete, giving up
-// after limit_ns or as soon as another warp of the CTA has given up.  With
-// `cluster_scope` the wait acquires at cluster scope (peers' writes made
-// before their release-arrive become visible).
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
-                                       bool cluster_scope) {
-  const uint64_t t0 = globaltimer_ns();
-  // Sleep in slices of at most 20 us (woken early when the phase completes),
-  // never past the wait's own limit.
-  const uint32_t hint = (uint32_t)(limit_ns < 20000ull ? limit_ns : 20000ull);
-  for (;;) {
-    if (cluster_scope ? mbar_try_wait_cluster_sleep(bar, parity, hint) : mbar_try_wait_sleep(bar, parity, hint))
-      return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 >= limit_ns) {
-      record_timeout(abort_flag);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                             volatile int* abort_flag, bool cluster_scope = false) {
-  if (cluster_scope ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, limit_ns, abort_flag, cluster_scope);
-}
-
-// Teardown wait: ignores the abort flag, gives up after limit_ns.
-__device__ __noinline__ void wait_teardown(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           uint64_t limit_ns = TEARDOWN_LIMIT_NS) {
-  if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 >= limit_ns) {
-      record_timeout(abort_flag);
-      return;
-    }
-  }
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void advance(uint32_t& stage, uint32_t& phase, uint32_t stages) {
-  if (++stage == stages) {
-    stage = 0;
-    phase ^= 1;
-  }
-}
 
 // Ranks of chunk j of group member `member`: [first, first + count).
 __device__ __forceinline__ void chunk_ranks(const Args& a, int member, int j, int& first, int& count) {
@@ -1245,72 +1185,6 @@ __global__ void __launch_bounds__(Cfg<PAIR, MX>::THREADS, 1)
   cluster_sync_all();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-  });
-  return fn;
-}
-
-// Row-major bf16 matrix [outer, inner] read as tiles of box_outer rows x 64
-// columns with the 128-byte swizzle; out-of-range rows read as zero.
-bool make_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t inner,
-              uint64_t outer, uint32_t box_outer) {
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * 2};
-  cuuint32_t box[2] = {(cuuint32_t)BK, box_outer};
-  cuuint32_t elem_strides[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Row-major codes [outer, inner bytes] (E4M3, or packed E2M1) read as tiles of
-// box_outer rows x 128 bytes with the 128-byte swizzle (the layout of the bf16 tiles above).
-bool make_map_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t inner,
-                    uint64_t outer, uint32_t box_outer) {
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner};
-  cuuint32_t box[2] = {(cuuint32_t)BKQ, box_outer};
-  cuuint32_t elem_strides[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// MXFP8 scales (the blocked layout of lg_mx_quantize) viewed as rows of 256
-// bytes: a 512-byte group is a box of two rows.  Groups past the end read as
-// zero.
-bool make_map_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t groups) {
-  cuuint64_t dims[2] = {256, groups * 2};
-  cuuint64_t strides[1] = {256};
-  cuuint32_t box[2] = {256, 2};
-  cuuint32_t elem_strides[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Row-major bf16 y [rows, cols] written in 32 x 32 boxes from 64-byte-swizzled
-// shared memory; the store clips rows and columns outside the matrix.
-bool make_store_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, void* base, uint64_t cols,
-                    uint64_t rows) {
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {(cuuint32_t)Y_BOX, (cuuint32_t)Y_BOX};
-  cuuint32_t elem_strides[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, elem_strides,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Launch geometry: down-projection chunking and stage count.  The h
 // exchange of a group reuses the start of the stage ring, so every stage of
 // shared memory goes to the ring.
@@ -1594,14 +1468,11 @@ cudaError_t read_and_clear_device_error(cudaStream_t s, int* value) {
   *value = 0;
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;
-  int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int));
+  e = take_device_error(value);
   if (e != cudaSuccess) return e;
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
-  }
-  *value = v;
+  int tile = 0;
+  e = take_tile_error(&tile);
+  if (*value == 0) *value = tile;
   return e;
 }
 
