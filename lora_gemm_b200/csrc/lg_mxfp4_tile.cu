@@ -89,6 +89,14 @@ struct Args {
   unsigned long long wait_limit_ns;
 };
 
+// wait_bounded, also for limits below the time that the hardware may hold a
+// plain try_wait by itself (a wait that short is polled from its start).
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
+                                             bool cluster_scope = false) {
+  if (limit_ns < 20000ull) return wait_slow(bar, parity, limit_ns, abort_flag, cluster_scope);
+  return wait_bounded(bar, parity, limit_ns, abort_flag, cluster_scope);
+}
+
 // Tile i: token panel p, column tile t; blocks of RASTER panels, panels fastest.
 __device__ __forceinline__ void tile_at(const Args& a, int i, int& p, int& t) {
   const int per = RASTER * a.n_tiles;
@@ -118,7 +126,7 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
     const int n0 = t * TN + (int)half * (int)C::B_ROWS;
     const int g0 = t * TN / 128;  // first scale group of the tile's columns
     for (int kb = 0; kb < a.q_stages; ++kb) {
-      if (!wait_bounded(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
+      if (!wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
         ok = false;
         break;
       }
@@ -149,7 +157,7 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
       waited = true;
     }
     for (int kb = 0; ok && kb < a.h_stages; ++kb) {
-      if (!wait_bounded(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
+      if (!wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
         ok = false;
         break;
       }
@@ -179,6 +187,19 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
   }
 }
 
+// Every lane's wait succeeded: the warp goes on, or gives up, as one.
+__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
+// The whole warp walks the stages and one elected lane issues: addresses and
+// descriptors stay warp-uniform values, which tcgen05 instructions take from
+// uniform registers.
 template <int TN>
 __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tmem, uint32_t cid, uint32_t ncl,
                          volatile int* abort_flag) {
@@ -197,10 +218,11 @@ __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tm
     // Columns of the tile start at row t TN of W: a multiple of 64, so up to
     // two scale columns (32 rows each) into the first group.
     const uint32_t sb_shift = (uint32_t)(t * TN % 128) / 32;
-    if (!wait_bounded(smem_u32(&ctl->acc_empty[buf]), (n / C::ACCS + 1) & 1, a.wait_limit_ns, abort_flag, true)) break;
+    if (!all_waited(wait_limited(smem_u32(&ctl->acc_empty[buf]), (n / C::ACCS + 1) & 1, a.wait_limit_ns, abort_flag, true)))
+      break;
     tc_fence_after();
     for (int kb = 0; kb < a.q_stages; ++kb) {
-      if (!wait_bounded(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag)) {
+      if (!all_waited(wait_limited(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag))) {
         ok = false;
         break;
       }
@@ -209,6 +231,7 @@ __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tm
       const uint64_t da = sw128_kmajor_desc(sa), db = sw128_kmajor_desc(sa + A_BYTES);
       const int groups = min(2, a.q_groups - 2 * kb);
       const uint32_t sf0 = tmem + C::SF_COL + C::SF_STAGE_COLS * sf_buf;
+      if (elect_lane()) {
       for (int g = 0; g < groups; ++g) {
         const uint32_t src = sa + A_BYTES + C::B_BYTES + (uint32_t)g * (1 + C::W_GROUPS) * SF_GROUP;
         const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
@@ -224,28 +247,35 @@ __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tm
                          (kb | g | k) != 0);
         }
       }
-      if (++sf_buf == C::SF_BUFS) sf_buf = 0;
       umma_commit_pair_mc(empty0 + 8 * stage, 3);
+      }
+      __syncwarp();
+      if (++sf_buf == C::SF_BUFS) sf_buf = 0;
       advance(stage, phase, stages);
     }
     for (int kb = 0; ok && kb < a.h_stages; ++kb) {
-      if (!wait_bounded(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag)) {
+      if (!all_waited(wait_limited(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag))) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t sa = smem + stage * C::STAGE;
       const uint64_t da = sw128_kmajor_desc(sa), db = sw128_kmajor_desc(sa + A_BYTES);
+      if (elect_lane()) {
 #pragma unroll
-      for (int k = 0; k < BK / 16; ++k) umma_ss_pair(d, da + 2 * k, db + 2 * k, idesc, (a.q_stages | kb | k) != 0);
-      umma_commit_pair_mc(empty0 + 8 * stage, 3);
+        for (int k = 0; k < BK / 16; ++k) umma_ss_pair(d, da + 2 * k, db + 2 * k, idesc, (a.q_stages | kb | k) != 0);
+        umma_commit_pair_mc(empty0 + 8 * stage, 3);
+      }
+      __syncwarp();
       advance(stage, phase, stages);
     }
     if (!ok) break;
-    umma_commit_pair_mc(smem_u32(&ctl->acc_full[buf]), 3);
+    if (elect_lane()) umma_commit_pair_mc(smem_u32(&ctl->acc_full[buf]), 3);
+    __syncwarp();
   }
   // Every MMA and copy must finish before TMEM is freed or either CTA exits.
-  umma_commit_pair_mc(smem_u32(&ctl->drain), 3);
+  if (elect_lane()) umma_commit_pair_mc(smem_u32(&ctl->drain), 3);
+  __syncwarp();
   wait_teardown(smem_u32(&ctl->drain), 0, abort_flag);
 }
 
@@ -268,7 +298,7 @@ __device__ void store_tiles(const CUtensorMap* tm_y, const Args& a, Control* ctl
     tile_at(a, i, p, t);
     const uint32_t buf = n % C::ACCS;
     if (!__all_sync(0xffffffffu,
-                    wait_bounded(acc_full0 + 8 * buf, (n / C::ACCS) & 1, a.wait_limit_ns, abort_flag)))
+                    wait_limited(acc_full0 + 8 * buf, (n / C::ACCS) & 1, a.wait_limit_ns, abort_flag)))
       break;
     tc_fence_after();
     uint32_t v[C::HALF / 32][32];
@@ -361,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0) produce<TN>(&tm_aq, &tm_bq, &tm_sa, &tm_sb, &tm_a, &tm_b, a, ctl, smem, half, cid, ncl, abort_flag);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && half == 0) multiply<TN>(a, ctl, smem, tmem, cid, ncl, abort_flag);
+    if (half == 0) multiply<TN>(a, ctl, smem, tmem, cid, ncl, abort_flag);
     __syncwarp();
   } else {
     store_tiles<TN>(&tm_y, a, ctl, smem, tmem, half, cid, ncl, warp, lane, abort_flag);

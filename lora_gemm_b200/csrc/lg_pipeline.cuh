@@ -118,12 +118,13 @@ inline bool make_map_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m
 }
 
 // MXFP8 scales (the blocked layout of lg_mx_quantize) viewed as rows of 256
-// bytes: a 512-byte group is a box of two rows.  Groups past the end read as
-// zero.
-inline bool make_map_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t groups) {
+// bytes: a 512-byte group is a box of two rows (box_rows: several groups in a
+// row).  Groups past the end read as zero.
+inline bool make_map_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t groups,
+                            uint32_t box_rows = 2) {
   cuuint64_t dims[2] = {256, groups * 2};
   cuuint64_t strides[1] = {256};
-  cuuint32_t box[2] = {256, 2};
+  cuuint32_t box[2] = {256, box_rows};
   cuuint32_t elem_strides[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
