@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr uint32_t B_ROWS = TN / 2;
   static constexpr uint32_t B_BYTES = B_ROWS * 128;
   static constexpr uint32_t SF_BYTES = 2 * (1 + W_GROUPS) * SF_GROUP;
-  static constexpr uint32_t STAGE = A_BYTES + B_BYTES + (SF_BYTES + 1023) / 1024 * 1024;
+  static constexpr uint32_t STAGE = A_BYTES + B_BYTES + SF_BYTES;
   static constexpr int HALF = TN / 2;  // accumulator columns per epilogue warp
   static_assert(TN % 64 == 0 && HALF % 32 == 0 && SF_BUFS >= 2 && 2 * SF_K <= SF_STAGE_COLS, "tile layout");
   static_assert(STAGE % 1024 == 0, "stages must stay 1024-byte aligned");
@@ -97,6 +97,16 @@ __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint
   return wait_bounded(bar, parity, limit_ns, abort_flag, cluster_scope);
 }
 
+// Every lane's wait succeeded: the warp goes on, or gives up, as one.
+__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // Tile i: token panel p, column tile t; blocks of RASTER panels, panels fastest.
 __device__ __forceinline__ void tile_at(const Args& a, int i, int& p, int& t) {
   const int per = RASTER * a.n_tiles;
@@ -126,29 +136,26 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
     const int n0 = t * TN + (int)half * (int)C::B_ROWS;
     const int g0 = t * TN / 128;  // first scale group of the tile's columns
     for (int kb = 0; kb < a.q_stages; ++kb) {
-      if (!wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
+      if (!all_waited(wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag))) {
         ok = false;
         break;
       }
       const uint32_t sa = smem + stage * C::STAGE;
       const uint32_t bar = full0 + 8 * stage;
-      const int groups = min(2, a.q_groups - 2 * kb);
-      if (half == 0) {
-        mbar_arrive_expect_tx(full_local + 8 * stage,
-                              2 * (A_BYTES + C::B_BYTES + (uint32_t)groups * (1 + C::W_GROUPS) * SF_GROUP));
-      }
-      tma_load_2d_pair(sa, tm_aq, bar, kb * 128, m0);
-      tma_load_2d_pair(sa + A_BYTES, tm_bq, bar, kb * 128, n0);
-      // Each CTA's tensor memory takes its own rows' scales and those of all
-      // the tile's columns.  A 512-byte group is two 256-byte rows of the map.
-      for (int g = 0; g < groups; ++g) {
-        const uint32_t sf = sa + A_BYTES + C::B_BYTES + (uint32_t)g * (1 + C::W_GROUPS) * SF_GROUP;
-        const int kg = 2 * kb + g;
-        tma_load_2d_pair(sf, tm_sa, bar, 0, 2 * ((m0 / BM) * a.q_groups + kg));
+      if (elect_lane()) {
+        if (half == 0) mbar_arrive_expect_tx(full_local + 8 * stage, 2 * (A_BYTES + C::B_BYTES + C::SF_BYTES));
+        tma_load_2d_pair(sa, tm_aq, bar, kb * 128, m0);
+        tma_load_2d_pair(sa + A_BYTES, tm_bq, bar, kb * 128, n0);
+        // Each CTA's tensor memory takes its own rows' scales and those of all
+        // the tile's columns, two 512-byte groups (four 256-byte rows of the
+        // map) at a time; past an odd last group: bytes that no MMA reads.
+        const uint32_t sf = sa + A_BYTES + C::B_BYTES;
+        tma_load_2d_pair(sf, tm_sa, bar, 0, 2 * ((m0 / BM) * a.q_groups + 2 * kb));
 #pragma unroll
         for (int w = 0; w < C::W_GROUPS; ++w)
-          tma_load_2d_pair(sf + (1 + w) * SF_GROUP, tm_sb, bar, 0, 2 * ((g0 + w) * a.q_groups + kg));
+          tma_load_2d_pair(sf + (1 + w) * 2 * SF_GROUP, tm_sb, bar, 0, 2 * ((g0 + w) * a.q_groups + 2 * kb));
       }
+      __syncwarp();
       ++fills;
       advance(stage, phase, stages);
     }
@@ -157,15 +164,18 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
       waited = true;
     }
     for (int kb = 0; ok && kb < a.h_stages; ++kb) {
-      if (!wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag)) {
+      if (!all_waited(wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag))) {
         ok = false;
         break;
       }
       const uint32_t sa = smem + stage * C::STAGE;
       const uint32_t bar = full0 + 8 * stage;
-      if (half == 0) mbar_arrive_expect_tx(full_local + 8 * stage, 2 * (A_BYTES + C::B_BYTES));
-      tma_load_2d_pair(sa, tm_a, bar, kb * BK, m0);
-      tma_load_2d_pair(sa + A_BYTES, tm_b, bar, kb * BK, n0);
+      if (elect_lane()) {
+        if (half == 0) mbar_arrive_expect_tx(full_local + 8 * stage, 2 * (A_BYTES + C::B_BYTES));
+        tma_load_2d_pair(sa, tm_a, bar, kb * BK, m0);
+        tma_load_2d_pair(sa + A_BYTES, tm_b, bar, kb * BK, n0);
+      }
+      __syncwarp();
       ++fills;
       advance(stage, phase, stages);
     }
@@ -187,19 +197,11 @@ __device__ void produce(const CUtensorMap* tm_aq, const CUtensorMap* tm_bq, cons
   }
 }
 
-// Every lane's wait succeeded: the warp goes on, or gives up, as one.
-__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
-
-// One lane of the (converged) warp, always the same.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t yes;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
-  return yes != 0;
-}
-
-// The whole warp walks the stages and one elected lane issues: addresses and
-// descriptors stay warp-uniform values, which tcgen05 instructions take from
-// uniform registers.
+// In both issuing warps all lanes walk the stages and one elected lane issues:
+// addresses and descriptors stay warp-uniform values, which TMA and tcgen05
+// instructions take from uniform registers.  (From a divergent lane every
+// operand is moved there first: a stage's eight loads alone then took 0.53 us,
+// twice its MMAs' time at any tile width.)
 template <int TN>
 __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tmem, uint32_t cid, uint32_t ncl,
                          volatile int* abort_flag) {
@@ -233,10 +235,10 @@ __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tm
       const uint32_t sf0 = tmem + C::SF_COL + C::SF_STAGE_COLS * sf_buf;
       if (elect_lane()) {
       for (int g = 0; g < groups; ++g) {
-        const uint32_t src = sa + A_BYTES + C::B_BYTES + (uint32_t)g * (1 + C::W_GROUPS) * SF_GROUP;
+        const uint32_t src = sa + A_BYTES + C::B_BYTES + (uint32_t)g * SF_GROUP;
         const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
 #pragma unroll
-        for (int w = 0; w < 1 + C::W_GROUPS; ++w) tmem_cp_32x128b_x4_pair(sf + 4 * w, plain_rows16_desc(src + w * SF_GROUP));
+        for (int w = 0; w < 1 + C::W_GROUPS; ++w) tmem_cp_32x128b_x4_pair(sf + 4 * w, plain_rows16_desc(src + 2 * w * SF_GROUP));
       }
       for (int g = 0; g < groups; ++g) {
         const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
@@ -388,8 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t tmem = ctl->tmem_base;
   volatile int* abort_flag = &ctl->abort_flag;
   if (warp == 0) {
-    if (lane == 0) produce<TN>(&tm_aq, &tm_bq, &tm_sa, &tm_sb, &tm_a, &tm_b, a, ctl, smem, half, cid, ncl, abort_flag);
-    __syncwarp();
+    produce<TN>(&tm_aq, &tm_bq, &tm_sa, &tm_sb, &tm_a, &tm_b, a, ctl, smem, half, cid, ncl, abort_flag);
   } else if (warp == 1) {
     if (half == 0) multiply<TN>(a, ctl, smem, tmem, cid, ncl, abort_flag);
     __syncwarp();
@@ -437,8 +438,8 @@ cudaError_t tile_launch(const Product& p, int pairs, uint64_t wait_limit_ns, cud
     const uint64_t groups = (uint64_t)p.q_k / BKQ;
     ok = ok && make_map_codes(enc, &tm_aq, p.aq, (uint64_t)p.q_k / 2, (uint64_t)p.M, BM) &&
          make_map_codes(enc, &tm_bq, p.bq, (uint64_t)p.q_k / 2, (uint64_t)p.N, C::B_ROWS) &&
-         make_map_scales(enc, &tm_sa, p.sa, (uint64_t)((p.M + 127) / 128) * groups) &&
-         make_map_scales(enc, &tm_sb, p.sb, (uint64_t)((p.N + 127) / 128) * groups);
+         make_map_scales(enc, &tm_sa, p.sa, (uint64_t)((p.M + 127) / 128) * groups, 4) &&
+         make_map_scales(enc, &tm_sb, p.sb, (uint64_t)((p.N + 127) / 128) * groups, 4);
   }
   if (p.bf16_k > 0) {
     ok = ok && make_map(enc, &tm_a, p.a, (uint64_t)p.bf16_k, (uint64_t)p.M, BM) &&
