@@ -483,7 +483,7 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
   p.sm_count = sms;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   if (mx) {
-    p.mx_bits = mx->bits;
+    p.mx = true;
     p.xq = mx->xq;
     p.xsf = mx->xsf;
     p.wq = mx->wq;
@@ -502,17 +502,13 @@ lg_status lora_linear_impl(const void* x, const void* W, const float* A_cat, con
     p.q_codes = sw->codes;
     p.q_scales = sw->scales;
   }
-  if (few) {
-    int kernels = 0;
-    const cudaError_t e = lg::launch_lora_linear_few(p, A_cat, B_cat, reinterpret_cast<uint16_t*>(workspace), &kernels, s);
-    if (e != cudaSuccess) cudaGetLastError();
-    return launched(e, (uint64_t)kernels);
-  }
   if (mx4) {
     int kernels = 0;
     bool failed = false;
-    uint16_t* h = R > 0 ? wsB + align256(2ull * N * R) / 2 : nullptr;
-    const cudaError_t e = lg::launch_lora_linear_tiles(p, h, &kernels, s, &failed);
+    uint16_t* h = R > 0 && !few ? wsB + align256(2ull * N * R) / 2 : nullptr;
+    const cudaError_t e =
+        few ? lg::launch_lora_linear_few(p, A_cat, B_cat, reinterpret_cast<float*>(workspace), &kernels, s, &failed)
+            : lg::launch_lora_linear_tiles(p, h, &kernels, s, &failed);
     if (e != cudaSuccess) cudaGetLastError();
     return launched(e, (uint64_t)kernels);
   }
@@ -573,7 +569,8 @@ lg_status lg_lora_linear_mxfp8(const void* x, const void* x_codes, const void* x
 }
 
 size_t lg_lora_linear_mxfp4_workspace_size(int64_t M, int K, int N, int R) {
-  // The bf16 factors and h [M, R] bf16 (few tokens: h alone, in their place).
+  // The bf16 factors and h [M, R] bf16.  Few tokens take h alone, in FP32, in
+  // the factors' place: 4 M R bytes, M <= 128, against 2 K R, K >= 128, and h's.
   const size_t factors = K % 128 ? 0 : lg_lora_linear_workspace_size(M, K, N, R);
   return factors == 0 ? 0 : factors + (size_t)align256(2ull * M * R);
 }

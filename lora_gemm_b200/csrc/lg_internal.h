@@ -107,11 +107,11 @@ struct LinearLaunch {
   int K, N, R;
   int sm_count;
   uint64_t wait_limit_ns;
-  // MX base term: E4M3 codes (mx_bits 8, lg_lora_linear_mxfp8) or packed E2M1
-  // codes (mx_bits 4, lg_lora_linear_mxfp4) and blocked E8M0 scales of x
-  // [M, K] and W [N, K]; x above stays the bf16 activations (the LoRA path
-  // reads them), W is unused.
-  int mx_bits = 0;
+  // MX base term: codes and blocked E8M0 scales of x [M, K] and W [N, K] --
+  // E4M3 for the panel kernel (mx, lg_lora_linear_mxfp8), packed E2M1 for the
+  // tile and few-token kernels (lg_lora_linear_mxfp4); x above stays the bf16
+  // activations (the LoRA path reads them), W is unused.
+  bool mx = false;
   const void* xq = nullptr;
   const void* xsf = nullptr;
   const void* wq = nullptr;
@@ -133,10 +133,10 @@ struct LinearLaunch {
 cudaError_t launch_lora_linear(const LinearLaunch& p, cudaStream_t s, bool* driver_failed);
 
 // lg_lora_linear_mxfp4 for few tokens: FP32 factors as they are, h a workspace
-// of M * R bf16 values.  *kernels: launches made.
+// of M * R floats.  *kernels: launches made.
 bool few_tokens(int64_t M);
-cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, const float* B_cat, uint16_t* h,
-                                   int* kernels, cudaStream_t s);
+cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, const float* B_cat, float* h,
+                                   int* kernels, cudaStream_t s, bool* driver_failed);
 
 // CTAs per cluster sharing one panel in lg_lora_linear (0: chosen per shape).
 void set_cluster_override(int g);
@@ -146,8 +146,9 @@ void set_variant_override(int v);
 // Device error word of the current device: read and clear (synchronous on s).
 cudaError_t read_and_clear_device_error(cudaStream_t s, int* value);
 
-// The same for the tile kernel's own error word (no synchronization before).
+// The same for the error words of the MXFP4 kernels (no synchronization before).
 cudaError_t take_tile_error(int* value);
+cudaError_t take_few_error(int* value);
 
 // lg_lora_linear_mxfp4 on output tiles: h = x A^T into `h` (workspace, M * R
 // bf16) and y = deq(x) deq(W)^T + h B^T, the factors in bf16.  *kernels:

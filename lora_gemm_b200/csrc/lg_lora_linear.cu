@@ -51,6 +51,7 @@
 //     copies and MMAs, frees its TMEM and returns.
 #include <atomic>
 #include <cstdlib>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda_fp8.h>
@@ -93,7 +94,7 @@ constexpr uint32_t Y_STAGE_BYTES = 8 * Y_WARP_BYTES;              // 16 KiB for 
 // reads them from there as an ordinary shared-memory A operand), which costs
 // one stage of the ring but gives every stage 7 % more work per byte.
 //
-// MX = 8 (pairs only): the base term x W^T runs as block-scaled MXFP8
+// MX = true (pairs only): the base term x W^T runs as block-scaled MXFP8
 // MMAs (tcgen05.mma kind::mxf8f6f4, E4M3 operands, one E8M0 scale per 32
 // values along K) over stages of 128 K elements -- the same 16 KiB x and W
 // tiles, plus the scale groups (512 bytes per 128 rows): each CTA's own 128
@@ -102,22 +103,10 @@ constexpr uint32_t Y_STAGE_BYTES = 8 * Y_WARP_BYTES;              // 16 KiB for 
 // (tcgen05.cp) before the stage's MMAs.  The scales take 32 TMEM columns (two
 // stages' worth of 4 + 8), so TMEM holds ranks [0, 448) of h and ranks
 // [448, 576) sit in two shared-memory tiles.
-//
-// MX = 4 (pairs only): the same with MXFP4 (tcgen05.mma kind::mxf4, E2M1
-// operands, two codes per byte): the 16 KiB tiles of a stage then hold 256 K
-// elements, i.e. two groups of scales, each with a slot and a tensor-memory
-// buffer of its own; an MMA takes K = 64 and two bytes of every scale word.
-// K is a multiple of 128: an odd number of groups leaves the last stage half
-// empty (the loads fill it with zeros, its MMAs are not issued).
-template <bool PAIR, int MX = 0>
+template <bool PAIR, bool MX = false>
 struct Cfg {
   static constexpr int BN = PAIR ? 256 : 224;                         // output columns per tile
-  static constexpr int SF_BUFS = MX ? 4 : 0;                            // scale buffers in TMEM, one per 128 K
-  // Scale slots in shared memory, one per 128 K.  MXFP4 stages take two: eight
-  // slots let the scales run as far ahead as the operand ring does.
-  static constexpr int SF_SLOTS = MX == 4 ? 8 : SF_BUFS;
-  static constexpr int STAGE_K = MX == 4 ? 256 : BKQ;                  // K elements of a base-term stage
-  static constexpr int STAGE_GROUPS = STAGE_K / BKQ;                   // scale groups of a base-term stage
+  static constexpr int SF_BUFS = MX ? 4 : 0;                            // MXFP8 scale buffers in TMEM
   static constexpr uint32_t SF_BUF_COLS = 16;                          // x 4 + W 2 x 4 columns, padded
   static constexpr uint32_t SF_COLS = (uint32_t)SF_BUFS * SF_BUF_COLS;  // TMEM columns for MXFP8 scales
   static constexpr uint32_t SF_COL = TMEM_COLS - SF_COLS;              // first of them
@@ -132,7 +121,7 @@ struct Cfg {
   // MX: the scales of a base-term stage (this CTA's x group, then both W
   // groups) travel in a ring of their own, one slot per scale buffer.
   static constexpr uint32_t SF_SLOT_BYTES = 2048;
-  static constexpr uint32_t SF_SLOTS_BYTES = MX ? (uint32_t)SF_SLOTS * SF_SLOT_BYTES : 0u;
+  static constexpr uint32_t SF_SLOTS_BYTES = MX ? (uint32_t)SF_BUFS * SF_SLOT_BYTES : 0u;
   static constexpr int MMA_M = PAIR ? 2 * BM : BM;
   // Warps: producer, MMA, 8 epilogue warps, and for MXFP8 a warp that copies
   // the scales of each stage into tensor memory ahead of the MMAs.
@@ -163,8 +152,8 @@ struct Control {
   uint64_t slice_ready;        // every group member's slice of h is in its staging rows
   uint64_t slice_free;         // every group member has copied this CTA's slice
   uint64_t epi_sync;           // all epilogue warps finished writing this panel's h slice
-  uint64_t sfl_full[8];        // MX: a scale slot's loads have landed (pair: counted on the leader)
-  uint64_t sfl_empty[8];       // MX: a scale slot has been copied to TMEM and may be refilled
+  uint64_t sfl_full[4];        // MXFP8: a scale slot's loads have landed (pair: counted on the leader)
+  uint64_t sfl_empty[4];       // MXFP8: a scale slot has been copied to TMEM and may be refilled
   uint64_t sf_full[4];         // MXFP8: a TMEM scale buffer holds its stage's scales (leader)
   uint64_t sf_empty[4];        // MXFP8: the MMAs that read a scale buffer are done (leader)
   uint64_t sf_drain;           // MXFP8: every scale copy has finished (leader)
@@ -180,8 +169,7 @@ struct Args {
   int num_panels;
   int n_tiles;
   int k_blocks;
-  int kq_blocks;  // MX: stages in the base-term loop (128 K elements each, MXFP4: 256)
-  int kq_groups;  // MX: scale groups of 128 K elements in K
+  int kq_blocks;  // MXFP8: stages of 128 K elements in the base-term loop
   int r_blocks;
   int group;        // members (CTAs, or pairs) sharing one panel
   int slice;        // ranks of h each member computes (R when group == 1)
@@ -263,7 +251,7 @@ __device__ __forceinline__ bool work_item(const Args& a, uint32_t cid, uint32_t 
 // x tiles loaded last are the first ones the next sweep of the same panel
 // re-reads, while they are still in L2.
 // ---------------------------------------------------------------------------
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ void run_producer(const CUtensorMap* tm_x, const CUtensorMap* tm_w, const CUtensorMap* tm_a,
                              const CUtensorMap* tm_b, const CUtensorMap* tm_xq, const CUtensorMap* tm_sfa,
                              const CUtensorMap* tm_sfb, const Args& a, Control* ctl, uint32_t smem_base,
@@ -352,39 +340,30 @@ __device__ void run_producer(const CUtensorMap* tm_x, const CUtensorMap* tm_w, c
         }
         const uint32_t sa = smem_base + stage * C::STAGE;
         if (posts_tx) mbar_arrive_expect_tx(full_local + 8 * stage, tx_k);
-        if constexpr (MX != 0) {
+        if constexpr (MX) {
           // E4M3 codes of x and W (128 K per stage), the scale group of this
           // CTA's x rows and both groups of the tile's 256 W rows: group
           // (row block, K block) is two 256-byte rows of the scale map.
           const int nb0 = a.ffn > 0 ? t : t * C::BN / BM;                 // row block of B rows 0-127
           const int nb1 = a.ffn > 0 ? a.ffn / BM + t : t * C::BN / BM + 1;  // ... and of rows 128-255
-          // Both formats fill a stage's 128-byte rows: coordinate 128 kb in bytes.
           load_x(tm_xq, sa, kb * BKQ, m0);
           load(tm_w, sa + A_BYTES, kb * BKQ, n0);
-          // The scales into their own slots, once the scale-copy warp has
-          // moved a slot's previous contents to tensor memory.
-#pragma unroll
-          for (int gi = 0; gi < C::STAGE_GROUPS; ++gi) {
-            const int kg = kb * C::STAGE_GROUPS + gi;
-            if (C::STAGE_GROUPS > 1 && kg >= a.kq_groups) break;
-            const uint32_t b = sf_fills % (uint32_t)C::SF_SLOTS;
-            if (!wait_bounded(sfl_empty0 + 8 * b, ((sf_fills / (uint32_t)C::SF_SLOTS) & 1u) ^ 1u, a.wait_limit_ns,
-                              abort_flag)) {
-              ok = false;
-              break;
-            }
-            const uint32_t slot = smem_base + a.sf_slot_off + b * C::SF_SLOT_BYTES;
-            if (posts_tx) mbar_arrive_expect_tx(sfl_full_local + 8 * b, tx_sf);
-            tma_load_2d_pair(slot, tm_sfa, sfl_full0 + 8 * b, 0, 2 * ((m0 / BM) * a.kq_groups + kg));
-            tma_load_2d_pair(slot + SF_GROUP_BYTES, tm_sfb, sfl_full0 + 8 * b, 0, 2 * (nb0 * a.kq_groups + kg));
-            tma_load_2d_pair(slot + 2 * SF_GROUP_BYTES, tm_sfb, sfl_full0 + 8 * b, 0, 2 * (nb1 * a.kq_groups + kg));
-            ++sf_fills;
-          }
-          if (!ok) {
+          // The scales into their own slot, once the scale-copy warp has
+          // moved the slot's previous contents to tensor memory.
+          const uint32_t b = sf_fills % (uint32_t)C::SF_BUFS;
+          if (!wait_bounded(sfl_empty0 + 8 * b, ((sf_fills / (uint32_t)C::SF_BUFS) & 1u) ^ 1u, a.wait_limit_ns,
+                            abort_flag)) {
+            ok = false;
             ++fills;
             advance(stage, phase, stages);
             break;
           }
+          const uint32_t slot = smem_base + a.sf_slot_off + b * C::SF_SLOT_BYTES;
+          if (posts_tx) mbar_arrive_expect_tx(sfl_full_local + 8 * b, tx_sf);
+          tma_load_2d_pair(slot, tm_sfa, sfl_full0 + 8 * b, 0, 2 * ((m0 / BM) * a.kq_blocks + kb));
+          tma_load_2d_pair(slot + SF_GROUP_BYTES, tm_sfb, sfl_full0 + 8 * b, 0, 2 * (nb0 * a.kq_blocks + kb));
+          tma_load_2d_pair(slot + 2 * SF_GROUP_BYTES, tm_sfb, sfl_full0 + 8 * b, 0, 2 * (nb1 * a.kq_blocks + kb));
+          ++sf_fills;
         } else {
           load_x(tm_x, sa, kb * BK, m0);
           load(tm_w, sa + A_BYTES, kb * BK, n0);
@@ -412,9 +391,9 @@ __device__ void run_producer(const CUtensorMap* tm_x, const CUtensorMap* tm_w, c
       const uint64_t fs = fills / stages + (s < fills % stages ? 1 : 0);
       if (fs) wait_teardown(full_local + 8 * s, (uint32_t)((fs - 1) & 1), abort_flag);
     }
-    if constexpr (MX != 0) {
-      for (uint32_t b = 0; b < (uint32_t)C::SF_SLOTS; ++b) {
-        const uint32_t fb = sf_fills / (uint32_t)C::SF_SLOTS + (b < sf_fills % (uint32_t)C::SF_SLOTS ? 1u : 0u);
+    if constexpr (MX) {
+      for (uint32_t b = 0; b < (uint32_t)C::SF_BUFS; ++b) {
+        const uint32_t fb = sf_fills / (uint32_t)C::SF_BUFS + (b < sf_fills % (uint32_t)C::SF_BUFS ? 1u : 0u);
         if (fb) wait_teardown(sfl_full_local + 8 * b, (fb - 1) & 1u, abort_flag);
       }
     }
@@ -430,7 +409,7 @@ __device__ void run_producer(const CUtensorMap* tm_x, const CUtensorMap* tm_w, c
 // ---------------------------------------------------------------------------
 // MMA issuer (warp 1, one thread; for pairs only the leader).
 // ---------------------------------------------------------------------------
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_t tmem, uint32_t crank, uint32_t cid,
                         uint32_t ncl, volatile int* abort_flag) {
   using C = Cfg<PAIR, MX>;
@@ -438,7 +417,6 @@ __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_
   const int member = PAIR ? (int)(crank >> 1) : (int)crank;
   const uint16_t mask = (uint16_t)(3u << (2 * member));
   uint32_t stage = 0, phase = 0, acc_phase = 0, sf_buf = 0;
-  uint32_t sweep = 0;  // as the producer counts them: odd sweeps run K backwards
   bool ok = true;
   const uint32_t full0 = smem_u32(&ctl->full[0]);
   const uint32_t empty0 = smem_u32(&ctl->empty[0]);
@@ -482,7 +460,7 @@ __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_
   const uint32_t a_rows = PAIR ? (uint32_t)a.chunk_n / 2 : (uint32_t)a.chunk_n;
   Work w;
   for (int k = 0; ok && work_item(a, cid, ncl, k, w); ++k) {
-    for (int j = 0; ok && j < a.n_chunks; ++j, ++sweep) {
+    for (int j = 0; ok && j < a.n_chunks; ++j) {
       if (!wait_bounded(acc_empty, acc_phase ^ 1, a.wait_limit_ns, abort_flag, PAIR)) {
         ok = false;
         break;
@@ -512,7 +490,7 @@ __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_
       commit(acc_full);
       acc_phase ^= 1;
     }
-    for (int t = w.t0 + member; ok && t < w.t1; t += a.group, ++sweep) {
+    for (int t = w.t0 + member; ok && t < w.t1; t += a.group) {
       if (!wait_bounded(acc_empty, acc_phase ^ 1, a.wait_limit_ns, abort_flag, PAIR)) {
         ok = false;
         break;
@@ -528,44 +506,27 @@ __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_
         const uint32_t sa = smem_base + stage * C::STAGE;
         const uint64_t da = sw128_kmajor_desc(sa);
         const uint64_t db = sw128_kmajor_desc(sa + A_BYTES);
-        if constexpr (MX != 0) {
+        if constexpr (MX) {
           // The scale-copy warp has put this stage's scales into TMEM scale
           // buffer sf_buf mod SF_BUFS (x rows in columns +0..3, W rows 0-127
           // in +4..7 and 128-255 in +8..11: row n's word sits in column
           // n / 32); once they are there, four K = 32 MMAs, the k-th taking
           // byte k of each row's scale word, and the buffer goes back to the
           // copy warp when they have completed.
-          // MXFP4: the same per group of 128 K, two K = 64 MMAs taking bytes
-          // 0-1 and 2-3 of the scale words.
-          const int kb = a.kq_groups & 1 ? ((sweep & 1) ? kloop - 1 - i : i) : 0;
-#pragma unroll
-          for (int gi = 0; gi < C::STAGE_GROUPS; ++gi) {
-            if (C::STAGE_GROUPS > 1 && kb * C::STAGE_GROUPS + gi >= a.kq_groups) break;
-            const uint32_t b = sf_buf % (uint32_t)C::SF_BUFS;
-            if (!wait_bounded(sf_full0 + 8 * b, (sf_buf / (uint32_t)C::SF_BUFS) & 1u, a.wait_limit_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sf = tmem + C::SF_COL + C::SF_BUF_COLS * b;
-            if constexpr (MX == 4) {
-#pragma unroll
-              for (int kk = 0; kk < BKQ / 64; ++kk) {
-                umma_mxf4_pair(d_acc, da + 2 * (2 * gi + kk), db + 2 * (2 * gi + kk),
-                               idesc_mxf4(C::MMA_M, C::BN, 2u * (uint32_t)kk, 2u * (uint32_t)kk), sf, sf + 4,
-                               (i | gi | kk) != 0);
-              }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < BKQ / 32; ++kk) {
-                umma_mx_pair(d_acc, da + 2 * kk, db + 2 * kk,
-                             idesc_mx_e4m3(C::MMA_M, C::BN, (uint32_t)kk, (uint32_t)kk), sf, sf + 4, (i | kk) != 0);
-              }
-            }
-            umma_commit_pair_mc(sf_empty0 + 8 * b, (uint16_t)(1u << crank));
-            ++sf_buf;
+          const uint32_t b = sf_buf % (uint32_t)C::SF_BUFS;
+          if (!wait_bounded(sf_full0 + 8 * b, (sf_buf / (uint32_t)C::SF_BUFS) & 1u, a.wait_limit_ns, abort_flag)) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sf = tmem + C::SF_COL + C::SF_BUF_COLS * b;
+#pragma unroll
+          for (int kk = 0; kk < BKQ / 32; ++kk) {
+            umma_mx_pair(d_acc, da + 2 * kk, db + 2 * kk, idesc_mx_e4m3(C::MMA_M, C::BN, (uint32_t)kk, (uint32_t)kk),
+                         sf, sf + 4, (i | kk) != 0);
+          }
+          umma_commit_pair_mc(sf_empty0 + 8 * b, (uint16_t)(1u << crank));
+          ++sf_buf;
         } else {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) mma_ss(da + 2 * kk, db + 2 * kk, idesc_y, (i | kk) != 0);
@@ -617,10 +578,10 @@ __device__ void run_mma(const Args& a, Control* ctl, uint32_t smem_base, uint32_
 // buffers let it work up to four stages ahead.  Its barriers count base-term
 // stages only, so it never waits on the operand ring.
 // ---------------------------------------------------------------------------
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ void run_scale_copies(const Args& a, Control* ctl, uint32_t smem_base, uint32_t tmem, uint32_t crank,
                                  uint32_t cid, uint32_t ncl, volatile int* abort_flag) {
-  if constexpr (MX != 0) {
+  if constexpr (MX) {
     using C = Cfg<PAIR, MX>;
     const int member = PAIR ? (int)(crank >> 1) : (int)crank;
     const uint32_t sfl_full0 = smem_u32(&ctl->sfl_full[0]);
@@ -631,28 +592,26 @@ __device__ void run_scale_copies(const Args& a, Control* ctl, uint32_t smem_base
     const uint16_t pair = (uint16_t)(3u << (crank & ~1u));
     uint32_t n = 0;
     bool ok = true;
-    const int kloop = a.fold ? 0 : a.kq_groups;
+    const int kloop = a.fold ? 0 : a.kq_blocks;
     Work w;
     for (int k = 0; ok && work_item(a, cid, ncl, k, w); ++k) {
       for (int t = w.t0 + member; ok && t < w.t1; t += a.group) {
         for (int i = 0; i < kloop; ++i, ++n) {
           const uint32_t b = n % (uint32_t)C::SF_BUFS;
           const uint32_t q = (n / (uint32_t)C::SF_BUFS) & 1u;
-          const uint32_t sl = n % (uint32_t)C::SF_SLOTS;
-          const uint32_t sq = (n / (uint32_t)C::SF_SLOTS) & 1u;
-          if (!wait_bounded(sfl_full0 + 8 * sl, sq, a.wait_limit_ns, abort_flag) ||
+          if (!wait_bounded(sfl_full0 + 8 * b, q, a.wait_limit_ns, abort_flag) ||
               !wait_bounded(sf_empty0 + 8 * b, q ^ 1u, a.wait_limit_ns, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t slot = smem_base + a.sf_slot_off + sl * C::SF_SLOT_BYTES;
+          const uint32_t slot = smem_base + a.sf_slot_off + b * C::SF_SLOT_BYTES;
           const uint32_t sf = tmem + C::SF_COL + C::SF_BUF_COLS * b;
           tmem_cp_32x128b_x4_pair(sf, plain_rows16_desc(slot));
           tmem_cp_32x128b_x4_pair(sf + 4, plain_rows16_desc(slot + SF_GROUP_BYTES));
           tmem_cp_32x128b_x4_pair(sf + 8, plain_rows16_desc(slot + 2 * SF_GROUP_BYTES));
           umma_commit_pair_mc(sf_full0 + 8 * b, self);
-          umma_commit_pair_mc(sfl_empty0 + 8 * sl, pair);
+          umma_commit_pair_mc(sfl_empty0 + 8 * b, pair);
         }
       }
     }
@@ -679,7 +638,7 @@ struct HRow {
   uint32_t sw;         // row mod 8
 };
 
-template <bool PAIR, int MX, int WORDS>
+template <bool PAIR, bool MX, int WORDS>
 __device__ __forceinline__ void h_put(const HRow& h, int r0, const uint32_t (&v)[WORDS]) {
   using C = Cfg<PAIR, MX>;
   if (!C::H_SMEM || r0 < C::R_TMEM) {
@@ -697,7 +656,7 @@ __device__ __forceinline__ void h_put(const HRow& h, int r0, const uint32_t (&v)
   }
 }
 
-template <bool PAIR, int MX, int WORDS>
+template <bool PAIR, bool MX, int WORDS>
 __device__ __forceinline__ void h_get(const HRow& h, int r0, uint32_t (&v)[WORDS]) {
   using C = Cfg<PAIR, MX>;
   if (!C::H_SMEM || r0 < C::R_TMEM) {
@@ -718,7 +677,7 @@ __device__ __forceinline__ void h_get(const HRow& h, int r0, uint32_t (&v)[WORDS
 
 // FP32 accumulator columns [0, count) = ranks first .. first+count-1 -> bf16
 // pairs in h.  count is a multiple of 8.
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ __forceinline__ void acc_to_h(const HRow& h, int first, int count, int half) {
   const int full_blocks = count / 16;
   for (int b = half; b < full_blocks; b += 2) {
@@ -743,7 +702,7 @@ __device__ __forceinline__ void acc_to_h(const HRow& h, int first, int count, in
 }
 
 // This member's slice of h (ranks s0 .. s0 + slice - 1) into its staging row.
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ __forceinline__ void h_to_staging(const HRow& h, int s0, int slice, int half, uint32_t row) {
   const int blocks = slice / 16;
   for (int b = half; b < blocks; b += 2) {
@@ -760,7 +719,7 @@ __device__ __forceinline__ void h_to_staging(const HRow& h, int s0, int slice, i
 }
 
 // A peer's staged slice (cluster address of its row) into this CTA's h.
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ __forceinline__ void staging_to_h(const HRow& h, int s0, int slice, int half, uint32_t remote_row) {
   const int blocks = slice / 16;
   for (int b = half; b < blocks; b += 2) {
@@ -866,7 +825,7 @@ __device__ __forceinline__ void euler_store(const Args& a, int64_t row, int col0
 // Epilogue (warps 2..9): warp w reads TMEM lanes 32 (w mod 4) .. +31 and
 // handles half (w - 2) / 4 of the columns.
 // ---------------------------------------------------------------------------
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __device__ void run_epilogue(const CUtensorMap* tm_y, const Args& a, Control* ctl, uint32_t smem_base, uint32_t tmem, uint32_t crank,
                              uint32_t cid, uint32_t ncl, int warp, int lane, volatile int* abort_flag) {
   using C = Cfg<PAIR, MX>;
@@ -963,7 +922,7 @@ __device__ void run_epilogue(const CUtensorMap* tm_y, const Args& a, Control* ct
       ok = __all_sync(0xffffffffu, wait_bounded(acc_full, acc_phase, a.wait_limit_ns, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      if constexpr (MX == 8) {
+      if constexpr (MX) {
         if (a.ffn > 0) {
           // Fused SwiGLU: accumulator columns [0, 128) are gate rows and
           // [128, 256) the matching up rows; this warp takes 64 of each.
@@ -979,7 +938,7 @@ __device__ void run_epilogue(const CUtensorMap* tm_y, const Args& a, Control* ct
           continue;
         }
       }
-      if constexpr (MX == 0) {
+      if constexpr (!MX) {
         if (a.eu_z) {
           // Euler output: this warp's y_n / 2 columns (a multiple of 8; a
           // 16-column load past them reads accumulator columns it ignores).
@@ -1074,7 +1033,7 @@ __device__ void run_epilogue(const CUtensorMap* tm_y, const Args& a, Control* ct
   __syncwarp();
 }
 
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 __global__ void __launch_bounds__(Cfg<PAIR, MX>::THREADS, 1)
     k_lora_linear(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                   const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -1105,11 +1064,9 @@ __global__ void __launch_bounds__(Cfg<PAIR, MX>::THREADS, 1)
     mbar_init(smem_u32(&ctl->slice_ready), EPI_WARPS * args.group);
     mbar_init(smem_u32(&ctl->slice_free), EPI_WARPS * args.group);
     mbar_init(smem_u32(&ctl->epi_sync), EPI_WARPS);
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(smem_u32(&ctl->sfl_full[b]), 1);
       mbar_init(smem_u32(&ctl->sfl_empty[b]), 1);
-    }
-    for (int b = 0; b < 4; ++b) {
       mbar_init(smem_u32(&ctl->sf_full[b]), 1);
       mbar_init(smem_u32(&ctl->sf_empty[b]), 1);
     }
@@ -1194,7 +1151,7 @@ struct Geometry {
   size_t smem = 0;
 };
 
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 bool make_geometry(int group, int R, Geometry* g) {
   using C = Cfg<PAIR, MX>;
   g->group = group;
@@ -1238,7 +1195,7 @@ int max_active_clusters(const void* kernel, int variant, int dev, int cluster, s
     bool known = false;
     int n = 0;
   };
-  static Entry cache[64][4][17];
+  static Entry cache[64][3][17];
   std::lock_guard<std::mutex> lock(mu);
   Entry* en = (dev >= 0 && dev < 64 && cluster <= 16) ? &cache[dev][variant - 1][cluster] : nullptr;
   if (en && en->known) return en->n;
@@ -1276,8 +1233,8 @@ cudaError_t configure_kernels(int dev) {
   unsigned long long ctx = 0;
   const bool have_ctx = current_context_id(&ctx);
   if (dev >= 0 && dev < 64 && have_ctx && configured[dev] && context[dev] == ctx) return cudaSuccess;
-  const void* kernels[4] = {(const void*)k_lora_linear<false, 0>, (const void*)k_lora_linear<true, 0>,
-                            (const void*)k_lora_linear<true, 8>, (const void*)k_lora_linear<true, 4>};
+  const void* kernels[3] = {(const void*)k_lora_linear<false, false>, (const void*)k_lora_linear<true, false>,
+                            (const void*)k_lora_linear<true, true>};
   for (const void* k : kernels) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1290,7 +1247,7 @@ cudaError_t configure_kernels(int dev) {
   return cudaSuccess;
 }
 
-template <bool PAIR, int MX>
+template <bool PAIR, bool MX>
 cudaError_t launch_variant(const LinearLaunch& p, cudaStream_t s, int dev, int cluster, bool* driver_failed,
                            PFN_cuTensorMapEncodeTiled_v12000 enc) {
   using C = Cfg<PAIR, MX>;
@@ -1307,13 +1264,12 @@ cudaError_t launch_variant(const LinearLaunch& p, cudaStream_t s, int dev, int c
   const bool fold = !MX && p.R > 0 && group == 1 && n_tiles == 1 && y_n <= C::FOLD_MAX_N &&
                     (a_rows + wf_rows) * BK * 2 <= C::B_BYTES;
   CUtensorMap tm_x, tm_w, tm_a, tm_b, tm_y, tm_xq, tm_sfa, tm_sfb;
-  bool ok = !p.x || make_map(enc, &tm_x, p.x, (uint64_t)p.K, (uint64_t)p.M, BM);
+  bool ok = make_map(enc, &tm_x, p.x, (uint64_t)p.K, (uint64_t)p.M, BM);
   if (MX) {
-    // Base term from the codes (rows of K bytes, MXFP4: K / 2) and scales;
-    // phase A still reads bf16 x.
-    const uint64_t kg = (uint64_t)(p.K / BKQ), row = (uint64_t)(p.K / C::STAGE_GROUPS);
-    ok = ok && make_map_codes(enc, &tm_w, p.wq, row, (uint64_t)p.N, C::B_ROWS) &&
-         make_map_codes(enc, &tm_xq, p.xq, row, (uint64_t)p.M, BM) &&
+    // Base term from the E4M3 codes and scales; phase A still reads bf16 x.
+    const uint64_t kg = (uint64_t)(p.K / BKQ);
+    ok = ok && make_map_codes(enc, &tm_w, p.wq, (uint64_t)p.K, (uint64_t)p.N, C::B_ROWS) &&
+         make_map_codes(enc, &tm_xq, p.xq, (uint64_t)p.K, (uint64_t)p.M, BM) &&
          make_map_scales(enc, &tm_sfa, p.xsf, (uint64_t)((p.M + BM - 1) / BM) * kg) &&
          make_map_scales(enc, &tm_sfb, p.wsf, (uint64_t)((p.N + BM - 1) / BM) * kg);
   } else {
@@ -1322,7 +1278,6 @@ cudaError_t launch_variant(const LinearLaunch& p, cudaStream_t s, int dev, int c
     tm_sfa = tm_x;
     tm_sfb = tm_x;
   }
-  if (MX && !p.x) tm_x = tm_xq;  // never read without ranks
   if (ok) {
     if (C::Y_TMA && p.ffn == 0 && !p.eu_z) {
       ok = make_store_map(enc, &tm_y, p.y, (uint64_t)p.N, (uint64_t)p.M);
@@ -1360,8 +1315,7 @@ cudaError_t launch_variant(const LinearLaunch& p, cudaStream_t s, int dev, int c
   args.q_codes = reinterpret_cast<uint8_t*>(p.q_codes);
   args.q_scales = reinterpret_cast<uint8_t*>(p.q_scales);
   args.k_blocks = p.K / BK;
-  args.kq_blocks = MX ? (p.K + C::STAGE_K - 1) / C::STAGE_K : 0;
-  args.kq_groups = MX ? p.K / BKQ : 0;
+  args.kq_blocks = MX ? p.K / BKQ : 0;
   args.r_blocks = p.R / BK;
   args.group = group;
   args.slice = geo.slice;
@@ -1376,7 +1330,7 @@ cudaError_t launch_variant(const LinearLaunch& p, cudaStream_t s, int dev, int c
   args.sf_slot_off = geo.sf_slot_off;
   args.wait_limit_ns = p.wait_limit_ns;
   const void* kernel = (const void*)k_lora_linear<PAIR, MX>;
-  int clusters = max_active_clusters(kernel, MX ? (MX == 8 ? 3 : 4) : (PAIR ? 2 : 1), dev, cluster, geo.smem, p.sm_count, C::THREADS);
+  int clusters = max_active_clusters(kernel, MX ? 3 : (PAIR ? 2 : 1), dev, cluster, geo.smem, p.sm_count, C::THREADS);
   if (clusters <= 0) clusters = p.sm_count / cluster;
   // No more clusters than (panel, tile) pairs: with fewer panels than
   // resident clusters the work list shares each panel's tiles among several
@@ -1442,37 +1396,37 @@ cudaError_t launch_lora_linear(const LinearLaunch& p, cudaStream_t s, bool* driv
     // few (one for N <= 224), so members sharing a panel would idle.  Pairs
     // for K > 2048 as above (each CTA loads half of every A_cat chunk).
     const int v = g_variant_override.load(std::memory_order_relaxed);
-    if (v == 1 || (v == 0 && p.K <= 2048)) return launch_variant<false, 0>(p, s, dev, 1, driver_failed, enc);
-    return launch_variant<true, 0>(p, s, dev, 2, driver_failed, enc);
+    if (v == 1 || (v == 0 && p.K <= 2048)) return launch_variant<false, false>(p, s, dev, 1, driver_failed, enc);
+    return launch_variant<true, false>(p, s, dev, 2, driver_failed, enc);
   }
-  if (p.mx_bits) {
-    // The MX base terms run on SM pairs only.
+  if (p.mx) {
+    // The MXFP8 base term runs on SM pairs only.
     if (g_variant_override.load(std::memory_order_relaxed) == 0 && g_cluster_override.load(std::memory_order_relaxed) == 0)
       cluster = p.K <= 4096 ? 2 : 4;
     if (cluster < 2) cluster = 2;
     if (cluster > 8) cluster = 8;
-    if (p.mx_bits == 4) return launch_variant<true, 4>(p, s, dev, cluster, driver_failed, enc);
-    return launch_variant<true, 8>(p, s, dev, cluster, driver_failed, enc);
+    return launch_variant<true, true>(p, s, dev, cluster, driver_failed, enc);
   }
   if (variant == 1) {
     if (cluster == 0) cluster = p.K <= 2048 ? 1 : 2;
     if (cluster > 8) cluster = 8;
-    return launch_variant<false, 0>(p, s, dev, cluster, driver_failed, enc);
+    return launch_variant<false, false>(p, s, dev, cluster, driver_failed, enc);
   }
   if (cluster < 2) cluster = 2;
   if (cluster > 8) cluster = 8;
-  return launch_variant<true, 0>(p, s, dev, cluster, driver_failed, enc);
+  return launch_variant<true, false>(p, s, dev, cluster, driver_failed, enc);
 }
 
 cudaError_t read_and_clear_device_error(cudaStream_t s, int* value) {
   *value = 0;
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;
-  e = take_device_error(value);
-  if (e != cudaSuccess) return e;
-  int tile = 0;
-  e = take_tile_error(&tile);
-  if (*value == 0) *value = tile;
+  for (auto take : {take_device_error, take_tile_error, take_few_error}) {
+    int v = 0;
+    e = take(&v);
+    if (e != cudaSuccess) return e;
+    if (*value == 0) *value = v;
+  }
   return e;
 }
 

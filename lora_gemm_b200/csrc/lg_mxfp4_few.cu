@@ -1,79 +1,51 @@
-// lg_lora_linear_mxfp4 for few tokens (M <= 64): bound by reading the weights
+// lg_lora_linear_mxfp4 for few tokens (M <= 128): bound by reading the weights
 // and factors once, 17/32 bytes per weight and 4 per factor.
 //
-// The panel kernel gives each SM pair a 256-token panel and computes
-// h = x A_cat^T once per panel and SM pair: with one panel that is every
-// pair reading all of A_cat, behind a pass that copies the factors to bf16
-// (1 x 7168 -> 7168, rank 576: 148 us, 6 % of HBM).  Here the weights are the
-// wide operand and the tokens the narrow one:
+// The tile kernel would multiply 256 token rows, give each SM pair whole
+// columns of K, and read the factors twice (a pass copies them to bf16): 65 x
+// 7168 -> 7168 at rank 576 takes it 53 us.  Here the weights are the wide
+// operand and the tokens the narrow one, and K is split:
 //
 //   k_few_down  h = x A_cat^T: a cluster of eight CTAs per 16 ranks, K spread
-//               over its 32 warps, partial sums joined through distributed
-//               shared memory.
-//   k_few_up    y = deq(x) deq(W)^T + h B_cat^T: a CTA per 32 outputs, K spread
-//               over its eight warps, each with a ring of cp.async stages of
-//               its own; the warps' sums are joined in a fixed order.
+//               over its 32 warps (mma.sync straight from registers: the FP32
+//               factors are rounded on the way, which no tensor-memory operand
+//               path does), partial sums joined through distributed shared
+//               memory.
+//   k_few_up    y = deq(x) deq(W)^T + h B_cat^T: 128 outputs per cluster of S
+//               CTAs that split K and the ranks; tcgen05 with the weights as the
+//               128-row operand and the tokens as its N (16 to 128): MXFP4
+//               stages of 256 K, then TF32 stages of 32 ranks that take B_cat
+//               and h as they are, in FP32.  All loads are TMA, 100 KB of them in
+//               flight per CTA; the CTAs' accumulators are joined in the order
+//               of their ranks through distributed shared memory.
 //
 // k_few_up is launched as a programmatic dependent: it reads weights while
-// k_few_down still runs and waits for h only before the adapters' term.
-//
-// The products run on mma.sync (m16n8k16, weights as the 16-row operand): at 8
-// to 64 tokens the warp's own registers feed it as fast as HBM delivers, without
-// the tensor-memory round trip, and a block's scale is applied to its FP32 sum.
-// E2M1 codes become f16 (exact); the sum of a block's 32 products is exact in
-// FP32 (multiples of 1/4 below 2^11), so the scales 2^(e_x + e_w) go in without
-// rounding.  K may be permuted freely within a block as long as both operands
-// agree: each lane takes eight consecutive codes, one 32-bit word.
+// k_few_down still runs and waits for h only before its first load of it.
 #include <cuda_bf16.h>
 
 #include "lg_internal.h"
+#include "lg_pipeline.cuh"
 
 namespace lg {
 
 namespace {
 
-constexpr int kUpWarps = 8;
-constexpr int kUpRows = 32;                   // outputs per CTA
-constexpr int kStageRows = kUpRows * 64;      // bytes of W codes per stage: 128 K
 constexpr int kDownWarps = 4;
 constexpr int kDownCluster = 8;
-constexpr int kDownRows = 16;                 // ranks per cluster
+constexpr int kDownRows = 16;  // ranks per cluster
 
-__device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
+constexpr int kUpRows = 128;     // outputs per cluster: the MMA's M
+constexpr int kUpThreads = 192;  // loads, MMAs, four epilogue warps
+constexpr int kUpStagesMax = 8;
+constexpr uint32_t kUpWBytes = kUpRows * 128;
+constexpr uint32_t kSfBytes = 1024;  // scales of 128 rows x 256 K
+
 __device__ __forceinline__ float4 ld_stream4(const float* p) {
   float4 v;
   asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "l"(p));
   return v;
-}
-
-// Eight E2M1 codes -> four f16 pairs, exact.
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
 }
 // FP32 values -> bf16 pairs, rounded to nearest (as the other layers round the
 // factors for the tensor cores).
@@ -87,12 +59,6 @@ __device__ __forceinline__ void round8(const float4& a, const float4& b, uint32_
   h[2] = round2(b.x, b.y);
   h[3] = round2(b.z, b.w);
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -100,278 +66,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// 2^(byte - 127): byte 0 is the subnormal 2^-127, 255 is NaN.
-__device__ __forceinline__ float e8m0(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
-}
-// All four scale bytes of a word are in [63, 190]: the product of two such
-// scales is 2^-128 .. 2^126, exact in FP32.
-__device__ __forceinline__ bool plain_scales(uint32_t w) {
-  const uint32_t v = w + 0x01010101u;
-  return ((v ^ (v << 1)) & 0x80808080u) == 0x80808080u;
-}
-
-struct UpArgs {
-  const uint8_t* xq;
-  const uint8_t* xsf;
-  const uint8_t* wq;
-  const uint8_t* wsf;
-  const float* B;       // [N, R]
-  const uint16_t* h;    // [M, R] bf16
-  uint16_t* y;
-  int M, K, N, R;
-};
-
-// NG: groups of eight tokens.
-template <int NG>
-struct UpCfg {
-  static constexpr int kX = NG * 8 * 64;                                // x codes per stage
-  static constexpr int kStage = kStageRows + kUpRows * 4 + kX + NG * 8 * 4;  // + W scale words, x scale words
-  // Two CTAs per SM (227 KB shared, 128 registers a thread) keep 16 warps and
-  // over 80 KB of copies in flight.
-  static constexpr int kStages = NG == 1 ? 4 : (NG <= 4 ? 3 : 2);
-  static constexpr int kWarp = kStage * kStages;
-  static constexpr int kSums = kUpWarps * kUpRows * NG * 8 * 4;
-  static constexpr int kSmem = kUpWarps * kWarp > kSums ? kUpWarps * kWarp : kSums;
-};
-
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-// (c, c1) += (d, d1) * s, two FP32 lanes in one instruction.
-__device__ __forceinline__ void fma2(float& c, float& c1, float d, float d1, uint64_t s) {
-  uint64_t v = pair2(c, c1);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(pair2(d, d1)), "l"(s));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(c), "=f"(c1) : "l"(v));
-}
-
-// One stage of 128 K: acc += deq(W) deq(x)^T.  PLAIN: every scale's exponent
-// field is in [63, 190] (plain_scales), so a scale is its byte in FP32's
-// exponent field and the product of two is exact.
-template <int NG, bool PLAIN>
-__device__ __forceinline__ void up_stage(uint32_t st, uint32_t xc, int g, int t, const uint32_t (&ws)[4],
-                                         const uint32_t (&xs)[NG][2], float (&acc)[2][NG][4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {  // the four blocks of 32
-    uint32_t w[4][4];
-    float sw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + g;
-      decode8(lds32(st + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), w[i]);
-      sw[i] = PLAIN ? __uint_as_float((c == 3 ? ws[i] >> 1 : ws[i] << (23 - 8 * c)) & 0x7F800000u)
-                    : e8m0((ws[i] >> (8 * c)) & 255u);
-    }
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      uint32_t x[4];
-      const int r = n * 8 + g;
-      decode8(lds32(xc + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4), x);
-      float sx[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sx[e] = PLAIN ? __uint_as_float((c == 3 ? xs[n][e] >> 1 : xs[n][e] << (23 - 8 * c)) & 0x7F800000u)
-                      : e8m0((xs[n][e] >> (8 * c)) & 255u);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x[0], x[1]);
-        mma_f16(d, w[2 * i][2], w[2 * i + 1][2], w[2 * i][3], w[2 * i + 1][3], x[2], x[3]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float(&o)[4] = acc[i][n];
-          const float s = sw[2 * i + e];
-          if (PLAIN) {
-            fma2(o[2 * e], o[2 * e + 1], d[2 * e], d[2 * e + 1], mul2(pair2(sx[0], sx[1]), pair2(s, s)));
-          } else {
-            // The smaller scale first: no step leaves FP32's range unless the
-            // result does.  (fminf drops a NaN, the sum s + sx keeps it.)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float lo = fminf(s, sx[k]), hi = s + sx[k] == s + sx[k] ? fmaxf(s, sx[k]) : s + sx[k];
-              o[2 * e + k] += (d[2 * e + k] * lo) * hi;
-            }
-          }
-        }
-      }
-    }
-  }
-}
-
-template <int NG>
-__global__ void __launch_bounds__(kUpWarps * 32, 2) k_few_up(const UpArgs a) {
-  using C = UpCfg<NG>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kUpRows;
-  // The steps of this CTA: groups of 128 K, then 16 ranks of the adapters'
-  // term each.  Warp w takes steps w, w + 8, ...
-  const int groups = a.K / 128;
-  const int steps = groups + a.R / 16;
-  const int64_t row_bytes = a.K / 2;
-  const uint32_t ring = s_addr(smem) + warp * C::kWarp;
-  bool waited = false;
-
-  // Stage layout: W codes [32 rows][64 B] (or 16 FP32 ranks of B_cat), 16-byte
-  // piece c of row r at c ^ ((r / 2) mod 4): no bank conflicts when eight rows
-  // are read at one piece; W scale words [32]; x codes [NG * 8][64 B] (or 32 B
-  // of h) likewise; x scale words.
-  constexpr uint32_t kWs = kStageRows, kXc = kWs + kUpRows * 4, kXs = kXc + C::kX;
-  auto fetch = [&](int step, int stage) {
-    const uint32_t st = ring + stage * C::kStage;
-    if (step < groups) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + g;
-        copy16(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.wq + (n0 + r) * row_bytes + step * 64 + t * 16);
-      }
-      // Row r of a group of 128 has its four scale bytes at 16 (r mod 32) + 4 (r / 32).
-      copy4(st + kWs + lane * 4,
-            a.wsf + (((int64_t)(n0 >> 7) * groups + step) << 9) + 16 * lane + 4 * ((n0 & 127) >> 5));
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int r = n * 8 + g;
-        if (r < a.M) copy16(st + kXc + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.xq + r * row_bytes + step * 64 + t * 16);
-      }
-#pragma unroll
-      for (int n = 0; n < (NG + 3) / 4; ++n) {
-        const int r = n * 32 + lane;
-        if (r < a.M && r < NG * 8) copy4(st + kXs + r * 4, a.xsf + ((int64_t)step << 9) + 16 * lane + 4 * n);
-      }
-    } else if (step < steps) {
-      const int r0 = (step - groups) * 16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + g;
-        copy16(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4), a.B + (int64_t)(n0 + r) * a.R + r0 + t * 4);
-      }
-      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is there
-      waited = true;
-#pragma unroll
-      for (int n = 0; n < (NG + 1) / 2; ++n) {
-        const int r = n * 16 + (lane >> 1), c = lane & 1;
-        if (r < a.M && r < NG * 8)
-          copy16(st + kXc + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), a.h + (int64_t)r * a.R + r0 + c * 8);
-      }
-    }
-    copy_commit();
-  };
-  // Tokens past M: codes (or h) 0 under scale 1, never overwritten.
-  for (int st = 0; st < C::kStages; ++st) {
-    uint8_t* base = smem + warp * C::kWarp + st * C::kStage;
-    for (int i = lane; i < C::kX / 16; i += 32) reinterpret_cast<uint4*>(base + kXc)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = lane; i < NG * 8; i += 32) reinterpret_cast<uint32_t*>(base + kXs)[i] = 0x7F7F7F7Fu;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int s = 0; s < C::kStages; ++s) fetch(warp + s * kUpWarps, s);
-
-  float acc[2][NG][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
-    }
-  }
-  int stage = 0;
-  for (int step = warp; step < steps; step += kUpWarps) {
-    copy_wait<C::kStages - 1>();
-    __syncwarp();  // every lane's pieces of this stage have landed
-    const uint32_t st = ring + stage * C::kStage;
-    if (step < groups) {
-      uint32_t ws[4];  // scale words of rows g, g + 8, g + 16, g + 24
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ws[i] = lds32(st + kWs + (i * 8 + g) * 4);
-      uint32_t xs[NG][2];  // of tokens 8 n + 2 t and + 1
-      bool plain = plain_scales(ws[0]) && plain_scales(ws[1]) && plain_scales(ws[2]) && plain_scales(ws[3]);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        xs[n][0] = lds32(st + kXs + (n * 8 + 2 * t) * 4);
-        xs[n][1] = lds32(st + kXs + (n * 8 + 2 * t + 1) * 4);
-        plain = plain && plain_scales(xs[n][0]) && plain_scales(xs[n][1]);
-      }
-      if (__all_sync(0xffffffffu, plain)) {
-        up_stage<NG, true>(st, st + kXc, g, t, ws, xs, acc);
-      } else {
-        up_stage<NG, false>(st, st + kXc, g, t, ws, xs, acc);
-      }
-    } else {
-      // 16 ranks: lane t has ranks 4 t .. 4 t + 3 of its rows and tokens.
-      uint32_t w[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + g;
-        float4 v;
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(st + r * 64 + ((t ^ ((r >> 1) & 3)) << 4))
-                     : "memory");
-        w[i][0] = round2(v.x, v.y);
-        w[i][1] = round2(v.z, v.w);
-      }
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int r = n * 8 + g;
-        uint32_t x0, x1;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(x0), "=r"(x1)
-                     : "r"(st + kXc + r * 64 + (((t >> 1) ^ ((r >> 1) & 3)) << 4) + (t & 1) * 8)
-                     : "memory");
-#pragma unroll
-        for (int i = 0; i < 2; ++i) mma_bf16(acc[i][n], w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1], x0, x1);
-      }
-    }
-    __syncwarp();  // the stage has been read by every lane
-    fetch(step + C::kStages * kUpWarps, stage);
-    if (++stage == C::kStages) stage = 0;
-  }
-  copy_wait<0>();
-  // Also where no adapter step was this warp's: the grid ends after k_few_down.
-  if (a.R > 0 && !waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // Join the warps' sums in their order: [warp][token][32 outputs].
-  __syncthreads();  // every warp is done with its ring
-  float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sums[(warp * NG * 8 + n * 8 + 2 * t + (e & 1)) * kUpRows + 16 * i + 8 * (e >> 1) + g] = acc[i][n][e];
-      }
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.M * (kUpRows / 2); i += kUpWarps * 32) {
-    const int m = i / (kUpRows / 2), r = i % (kUpRows / 2) * 2;
-    float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kUpWarps; ++w) {
-      const float2 p = *reinterpret_cast<const float2*>(&sums[(w * NG * 8 + m) * kUpRows + r]);
-      v.x += p.x;
-      v.y += p.y;
-    }
-    *reinterpret_cast<__nv_bfloat162*>(a.y + (int64_t)m * a.N + n0 + r) = __floats2bfloat162_rn(v.x, v.y);
-  }
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 struct DownArgs {
   const uint16_t* x;  // [M, K] bf16
   const float* A;     // [R, K]
-  uint16_t* h;        // [M, R] bf16
+  float* h;           // [M, R]
   int M, K, R;
 };
 
@@ -416,7 +118,7 @@ __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarp
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[warp][n * 8 + 2 * t + (e & 1)][8 * (e >> 1) + g] = acc[n][e];
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_barrier();
   // Each CTA joins an eighth of the cluster's M x 16 sums, CTA by CTA and warp
   // by warp.
   for (int i = (int)rank * kDownWarps * 32 + threadIdx.x; i < a.M * kDownRows; i += kDownCluster * kDownWarps * 32) {
@@ -425,7 +127,7 @@ __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarp
 #pragma unroll
     for (int c = 0; c < kDownCluster; ++c) {
       uint32_t peer;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(s_addr(&sums[0][m][r])), "r"(c));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_u32(&sums[0][m][r])), "r"(c));
 #pragma unroll
       for (int w = 0; w < kDownWarps; ++w) {
         float p;
@@ -436,58 +138,318 @@ __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarp
         v += p;
       }
     }
-    // Rounded to bf16 as the other layers round h for the up-projection.
-    a.h[(int64_t)m * a.R + r0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    a.h[(int64_t)m * a.R + r0 + r] = v;
   }
   // No CTA leaves while a peer may still read its sums.
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_barrier();
+}
+
+// NT: tokens, rounded up to the MMA's N.
+template <int NT>
+struct UpCfg {
+  static constexpr uint32_t kX = NT * 128;
+  static constexpr uint32_t kStage = kUpWBytes + kX + 2 * kSfBytes;
+  // Two CTAs per SM.
+  static constexpr int kStages = (int)(104 * 1024 / kStage) < kUpStagesMax ? (int)(104 * 1024 / kStage) : kUpStagesMax;
+  static constexpr uint32_t kSums = NT * kUpRows * 4;  // over the ring, once it is done
+  static constexpr uint32_t kRing = kStage * kStages > kSums ? kStage * kStages : kSums;
+  static constexpr uint32_t kSfCols = 16;  // TMEM columns of a stage's scales: W at 4 g, x at 8 + 4 g
+  static constexpr uint32_t kSfBufs = 4;
+  static constexpr uint32_t kCols = NT + kSfBufs * kSfCols <= 128 ? 128 : 256;  // TMEM columns allocated
+  static_assert(NT + kSfBufs * kSfCols <= kCols && kStages >= 3, "few-token layout");
+};
+
+struct UpControl {
+  uint64_t full[kUpStagesMax];
+  uint64_t empty[kUpStagesMax];
+  uint64_t done;  // every MMA has finished
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct UpArgs {
+  uint16_t* y;
+  int M, N;
+  int q_stages, q_groups;  // 256-K stages of the base term, 128-K scale groups
+  int h_stages;            // 32-rank stages of the adapters' term
+  unsigned long long wait_limit_ns;
+};
+
+// CTA `rank` of a cluster of S takes stages rank, rank + S, ... of the base term,
+// then of the adapters' term.
+template <int NT>
+__global__ void __launch_bounds__(kUpThreads)
+    k_few_up(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+             const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sx,
+             const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_h, const UpArgs a) {
+  using C = UpCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  UpControl* ctl = reinterpret_cast<UpControl*>(base + C::kRing);
+  const uint32_t smem = smem_u32(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t S;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  const uint32_t rank = cluster_ctarank();
+  const int tile = (int)cluster_id_x();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->done), 1);
+    ctl->abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), C::kCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]), done = smem_u32(&ctl->done);
+  const uint32_t stages = (uint32_t)C::kStages;
+
+  if (warp == 0) {
+    uint32_t stage = 0, phase = 0;
+    uint64_t fills = 0;
+    bool ok = true;
+    for (int kb = (int)rank; kb < a.q_stages; kb += (int)S) {
+      if (!all_waited(wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const uint32_t st = smem + stage * C::kStage, bar = full0 + 8 * stage;
+      if (elect_lane()) {
+        mbar_arrive_expect_tx(bar, C::kStage);
+        tma_load_2d(st, &tm_w, bar, kb * 128, tile * kUpRows);
+        tma_load_2d(st + kUpWBytes, &tm_x, bar, kb * 128, 0);
+        // Two 512-byte groups each; past an odd last group: bytes that no MMA reads.
+        tma_load_2d(st + kUpWBytes + C::kX, &tm_sw, bar, 0, 2 * (tile * a.q_groups + 2 * kb));
+        tma_load_2d(st + kUpWBytes + C::kX + kSfBytes, &tm_sx, bar, 0, 2 * (2 * kb));
+      }
+      __syncwarp();
+      ++fills;
+      advance(stage, phase, stages);
+    }
+    // Also where no stage needs h: the grid does not end before k_few_down.
+    if (a.h_stages > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int kb = (int)rank; ok && kb < a.h_stages; kb += (int)S) {
+      if (!all_waited(wait_limited(empty0 + 8 * stage, phase ^ 1, a.wait_limit_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const uint32_t st = smem + stage * C::kStage, bar = full0 + 8 * stage;
+      if (elect_lane()) {
+        mbar_arrive_expect_tx(bar, kUpWBytes + C::kX);
+        tma_load_2d(st, &tm_b, bar, kb * 32, tile * kUpRows);
+        tma_load_2d(st + kUpWBytes, &tm_h, bar, kb * 32, 0);
+      }
+      __syncwarp();
+      ++fills;
+      advance(stage, phase, stages);
+    }
+    // Every copy has landed before the ring is used for the sums.
+    for (uint32_t s = 0; s < stages; ++s) {
+      const uint64_t fs = fills / stages + (s < fills % stages ? 1 : 0);
+      if (fs) wait_teardown(full0 + 8 * s, (uint32_t)((fs - 1) & 1), abort_flag);
+    }
+  } else if (warp == 1) {
+    uint32_t stage = 0, phase = 0, sf_buf = 0;
+    uint32_t any = 0;  // 0 until the first MMA, which clears the accumulator
+    bool ok = true;
+    for (int kb = (int)rank; kb < a.q_stages; kb += (int)S) {
+      if (!all_waited(wait_limited(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = smem + stage * C::kStage;
+      const uint64_t dw = sw128_kmajor_desc(st), dx = sw128_kmajor_desc(st + kUpWBytes);
+      const uint32_t sf = tmem + NT + C::kSfCols * sf_buf;
+      const uint32_t src = st + kUpWBytes + C::kX;
+      const int groups = min(2, a.q_groups - 2 * kb);
+      if (elect_lane()) {
+        for (int g = 0; g < groups; ++g) {
+          tmem_cp_32x128b_x4(sf + 4 * g, plain_rows16_desc(src + g * 512));
+          tmem_cp_32x128b_x4(sf + 8 + 4 * g, plain_rows16_desc(src + kSfBytes + g * 512));
+        }
+        for (int g = 0; g < groups; ++g) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            umma_mxf4(tmem, dw + 2 * (2 * g + k), dx + 2 * (2 * g + k), idesc_mxf4(kUpRows, NT, 2u * k, 2u * k),
+                      sf + 4 * g, sf + 8 + 4 * g, any | (uint32_t)(g | k));
+          }
+        }
+        umma_commit(empty0 + 8 * stage);
+      }
+      __syncwarp();
+      any = 1;
+      if (++sf_buf == C::kSfBufs) sf_buf = 0;
+      advance(stage, phase, stages);
+    }
+    for (int kb = (int)rank; ok && kb < a.h_stages; kb += (int)S) {
+      if (!all_waited(wait_limited(full0 + 8 * stage, phase, a.wait_limit_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = smem + stage * C::kStage;
+      const uint64_t dw = sw128_kmajor_desc(st), dx = sw128_kmajor_desc(st + kUpWBytes);
+      if (elect_lane()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // K = 8 each: 32 bytes
+          umma_tf32(tmem, dw + 2 * k, dx + 2 * k, idesc_tf32(kUpRows, NT), any | (uint32_t)k);
+        umma_commit(empty0 + 8 * stage);
+      }
+      __syncwarp();
+      any = 1;
+      advance(stage, phase, stages);
+    }
+    if (elect_lane()) umma_commit(done);
+    __syncwarp();
+  }
+  // Every MMA has finished and every load has landed: the ring is free.
+  wait_teardown(done, 0, abort_flag, a.wait_limit_ns + TEARDOWN_LIMIT_NS);
+  __syncthreads();
+  tc_fence_after();
+  const bool some = (int)rank < a.q_stages || (int)rank < a.h_stages;  // this CTA had a stage
+  if (warp >= 2) {
+    const int row = 32 * (warp & 3) + lane;  // TMEM lane: output row of the tile
+    float* sums = reinterpret_cast<float*>(base) + row;
+#pragma unroll
+    for (int c = 0; c < NT / 16; ++c) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[(16 * c + i) * kUpRows] = some ? __uint_as_float(v[i]) : 0.f;
+    }
+    tc_fence_before();
+  }
+  cluster_barrier();
+  // Token m goes to CTA m mod S: four outputs per lane, summed in rank order.
+  for (int m = (int)rank + (int)S * warp; m < a.M; m += (int)S * (kUpThreads / 32)) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t at = smem + (uint32_t)(m * kUpRows + 4 * lane) * 4;
+    for (uint32_t c = 0; c < S; ++c) {
+      uint32_t p[4];
+      ld_shared_cluster_v4(mapa_shared(at, c), p[0], p[1], p[2], p[3]);
+      t.x += __uint_as_float(p[0]);
+      t.y += __uint_as_float(p[1]);
+      t.z += __uint_as_float(p[2]);
+      t.w += __uint_as_float(p[3]);
+    }
+    const int n = tile * kUpRows + 4 * lane;
+    if (n < a.N) *reinterpret_cast<uint2*>(a.y + (int64_t)m * a.N + n) = make_uint2(round2(t.x, t.y), round2(t.z, t.w));
+  }
+  // No CTA leaves while a peer may still read its sums.
+  cluster_barrier();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// CTAs that split a row tile's stages: as many as two per SM hold, of at least
+// three stages each.
+int up_split(int tiles, int steps, int sm_count) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= 2 * sm_count && steps >= 3 * 2 * s) s *= 2;
+  return s;
+}
+
+template <int NT>
+cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h, cudaStream_t s, bool* driver_failed,
+                      PFN_cuTensorMapEncodeTiled_v12000 enc) {
+  using C = UpCfg<NT>;
+  CUtensorMap tm_w, tm_x, tm_sw, tm_sx, tm_b, tm_h;
+  const uint64_t groups = (uint64_t)p.K / BKQ;
+  bool ok = make_map_codes(enc, &tm_w, p.wq, (uint64_t)p.K / 2, (uint64_t)p.N, kUpRows) &&
+            make_map_codes(enc, &tm_x, p.xq, (uint64_t)p.K / 2, (uint64_t)p.M, NT) &&
+            make_map_scales(enc, &tm_sw, p.wsf, (uint64_t)((p.N + 127) / 128) * groups, 4) &&
+            make_map_scales(enc, &tm_sx, p.xsf, (uint64_t)((p.M + 127) / 128) * groups, 4);
+  tm_b = tm_h = tm_w;  // never read without adapters
+  if (p.R > 0) {
+    ok = ok && make_map_fp32(enc, &tm_b, B_cat, (uint64_t)p.R, (uint64_t)p.N, kUpRows) &&
+         make_map_fp32(enc, &tm_h, h, (uint64_t)p.R, (uint64_t)p.M, NT);
+  }
+  if (!ok) {
+    *driver_failed = true;
+    return cudaErrorInvalidValue;
+  }
+  UpArgs a;
+  a.y = reinterpret_cast<uint16_t*>(p.y);
+  a.M = (int)p.M;
+  a.N = p.N;
+  a.q_stages = (p.K + 255) / 256;
+  a.q_groups = (int)groups;
+  a.h_stages = p.R / 32;
+  a.wait_limit_ns = p.wait_limit_ns;
+  constexpr int smem = (int)(1024 + C::kRing + sizeof(UpControl));
+  // A constant, so that calls from several host threads cannot lower it.
+  cudaError_t e = cudaFuncSetAttribute((const void*)k_few_up<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.N + kUpRows - 1) / kUpRows;
+  const int split = up_split(tiles, a.q_stages + a.h_stages, p.sm_count);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
+  cfg.blockDim = dim3(kUpThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.R > 0 ? 2 : 1;  // without adapters nothing waits for the kernel before
+  return cudaLaunchKernelEx(&cfg, k_few_up<NT>, tm_w, tm_x, tm_sw, tm_sx, tm_b, tm_h, a);
 }
 
 template <int NG>
-cudaError_t few_launch(const LinearLaunch& p, const float* A_cat, const float* B_cat, uint16_t* h, int* kernels,
-                       cudaStream_t s) {
-  using C = UpCfg<NG>;
-  *kernels = 0;
-  // A constant, so that calls from several host threads cannot lower it.
-  cudaError_t e = cudaFuncSetAttribute((const void*)k_few_up<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  if (p.R > 0) {
-    const DownArgs d{reinterpret_cast<const uint16_t*>(p.x), A_cat, h, (int)p.M, p.K, p.R};
-    k_few_down<NG><<<p.R / kDownRows * kDownCluster, kDownWarps * 32, 0, s>>>(d);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    *kernels = 1;
-  }
-  const UpArgs u{reinterpret_cast<const uint8_t*>(p.xq), reinterpret_cast<const uint8_t*>(p.xsf),
-                 reinterpret_cast<const uint8_t*>(p.wq), reinterpret_cast<const uint8_t*>(p.wsf),
-                 B_cat, h, reinterpret_cast<uint16_t*>(p.y), (int)p.M, p.K, p.N, p.R};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.N / kUpRows), 1, 1);
-  cfg.blockDim = dim3(kUpWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.R > 0 ? 1 : 0;  // without adapters nothing waits for the kernel before
-  e = cudaLaunchKernelEx(&cfg, k_few_up<NG>, u);
-  if (e == cudaSuccess) *kernels += 1;
-  return e;
+cudaError_t down_launch(const LinearLaunch& p, const float* A_cat, float* h, cudaStream_t s) {
+  const DownArgs d{reinterpret_cast<const uint16_t*>(p.x), A_cat, h, (int)p.M, p.K, p.R};
+  k_few_down<NG><<<p.R / kDownRows * kDownCluster, kDownWarps * 32, 0, s>>>(d);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-bool few_tokens(int64_t M) { return M <= 64; }
+cudaError_t take_few_error(int* value) { return take_device_error(value); }
 
-cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, const float* B_cat, uint16_t* h,
-                                   int* kernels, cudaStream_t s) {
-  if (p.M <= 8) return few_launch<1>(p, A_cat, B_cat, h, kernels, s);
-  if (p.M <= 16) return few_launch<2>(p, A_cat, B_cat, h, kernels, s);
-  if (p.M <= 24) return few_launch<3>(p, A_cat, B_cat, h, kernels, s);
-  if (p.M <= 32) return few_launch<4>(p, A_cat, B_cat, h, kernels, s);
-  if (p.M <= 48) return few_launch<6>(p, A_cat, B_cat, h, kernels, s);
-  return few_launch<8>(p, A_cat, B_cat, h, kernels, s);
+bool few_tokens(int64_t M) { return M <= 128; }
+
+cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, const float* B_cat, float* h,
+                                   int* kernels, cudaStream_t s, bool* driver_failed) {
+  *kernels = 0;
+  *driver_failed = false;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) {
+    *driver_failed = true;
+    return cudaErrorNotSupported;
+  }
+  cudaError_t e = cudaSuccess;
+  if (p.R > 0) {
+    if (p.M <= 8) e = down_launch<1>(p, A_cat, h, s);
+    else if (p.M <= 16) e = down_launch<2>(p, A_cat, h, s);
+    else if (p.M <= 32) e = down_launch<4>(p, A_cat, h, s);
+    else if (p.M <= 64) e = down_launch<8>(p, A_cat, h, s);
+    else e = down_launch<16>(p, A_cat, h, s);
+    if (e != cudaSuccess) return e;
+    *kernels = 1;
+  }
+  if (p.M <= 16) e = up_launch<16>(p, B_cat, h, s, driver_failed, enc);
+  else if (p.M <= 32) e = up_launch<32>(p, B_cat, h, s, driver_failed, enc);
+  else if (p.M <= 64) e = up_launch<64>(p, B_cat, h, s, driver_failed, enc);
+  else e = up_launch<128>(p, B_cat, h, s, driver_failed, enc);
+  if (e == cudaSuccess) *kernels += 1;
+  return e;
 }
 
 }  // namespace lg

@@ -89,24 +89,6 @@ struct Args {
   unsigned long long wait_limit_ns;
 };
 
-// wait_bounded, also for limits below the time that the hardware may hold a
-// plain try_wait by itself (a wait that short is polled from its start).
-__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
-                                             bool cluster_scope = false) {
-  if (limit_ns < 20000ull) return wait_slow(bar, parity, limit_ns, abort_flag, cluster_scope);
-  return wait_bounded(bar, parity, limit_ns, abort_flag, cluster_scope);
-}
-
-// Every lane's wait succeeded: the warp goes on, or gives up, as one.
-__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
-
-// One lane of the (converged) warp, always the same.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t yes;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
-  return yes != 0;
-}
-
 // Tile i: token panel p, column tile t; blocks of RASTER panels, panels fastest.
 __device__ __forceinline__ void tile_at(const Args& a, int i, int& p, int& t) {
   const int per = RASTER * a.n_tiles;

@@ -66,6 +66,24 @@ __device__ __noinline__ void wait_teardown(uint32_t bar, uint32_t parity, volati
   }
 }
 
+// wait_bounded, also for limits below the time that the hardware may hold a
+// plain try_wait by itself (a wait that short is polled from its start).
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
+                                             bool cluster_scope = false) {
+  if (limit_ns < 20000ull) return wait_slow(bar, parity, limit_ns, abort_flag, cluster_scope);
+  return wait_bounded(bar, parity, limit_ns, abort_flag, cluster_scope);
+}
+
+// Every lane's wait succeeded: the warp goes on, or gives up, as one.
+__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -117,7 +135,20 @@ inline bool make_map_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// MXFP8 scales (the blocked layout of lg_mx_quantize) viewed as rows of 256
+// Row-major FP32 matrix [outer, inner] read as tiles of box_outer rows x 32
+// columns with the 128-byte swizzle; out-of-range rows read as zero.
+inline bool make_map_fp32(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t inner,
+                          uint64_t outer, uint32_t box_outer) {
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner * 4};
+  cuuint32_t box[2] = {32, box_outer};
+  cuuint32_t elem_strides[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// MX scales (the blocked layout of lg_mx_quantize) viewed as rows of 256
 // bytes: a 512-byte group is a box of two rows (box_rows: several groups in a
 // row).  Groups past the end read as zero.
 inline bool make_map_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t groups,
