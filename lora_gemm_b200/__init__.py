@@ -203,12 +203,18 @@ def _same_device(ref, *tensors):
             raise ValueError(f"all tensors must be on {ref.device}, got one on {t.device}")
 
 
+def _addr(t):
+    """A tensor's address as ctypes takes it for a pointer argument (None for null)."""
+    return None if t is None else t.data_ptr()
+
+
 def _launch(device, fn, *args):
     """fn(*args, current stream of device), with device current."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(device))
+    index = device.index
+    if index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device):
-        return fn(*args, _stream(device))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _scales(pair, rows, K, what):
@@ -507,16 +513,16 @@ def mxfp4_quantize(x, codes=None, scales=None):
     rows, K = x.shape
     nscales = mx_scale_bytes(rows, K)
     if codes is None:
-        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
     else:
         _need(codes, torch.uint8, "codes", 2)
         _shape(codes, (rows, K // 2), "codes")
     if scales is None:
-        scales = torch.empty(nscales, dtype=torch.uint8, device=x.device)
+        scales = x.new_empty(nscales, dtype=torch.uint8)
     else:
         _at_least(scales, nscales, "scales")
     _same_device(x, codes, scales)
-    _check(_launch(x.device, lib.lg_mxfp4_quantize, _ptr(x), rows, K, _ptr(codes), _ptr(scales)), "lg_mxfp4_quantize")
+    _check(_launch(x.device, lib.lg_mxfp4_quantize, _addr(x), rows, K, _addr(codes), _addr(scales)), "lg_mxfp4_quantize")
     return codes, scales
 
 
@@ -526,12 +532,12 @@ def mxfp4_dequantize(codes, scales, out=None):
     rows, K = codes.shape[0], 2 * codes.shape[1]
     _at_least(scales, mx_scale_bytes(rows, K), "scales")
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
+        out = codes.new_empty((rows, K), dtype=torch.bfloat16)
     else:
         _need(out, torch.bfloat16, "out", 2)
         _shape(out, (rows, K), "out")
     _same_device(codes, scales, out)
-    _check(_launch(codes.device, lib.lg_mxfp4_dequantize, _ptr(codes), _ptr(scales), rows, K, _ptr(out)),
+    _check(_launch(codes.device, lib.lg_mxfp4_dequantize, _addr(codes), _addr(scales), rows, K, _addr(out)),
            "lg_mxfp4_dequantize")
     return out
 
@@ -567,19 +573,19 @@ def lora_linear_mxfp4(x, x_mx, W_mx, A_cat, B_cat, y=None, workspace=None):
         _need(x, torch.bfloat16, "x", 2)
         _shape(x, (M, K), "x")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        y = xq.new_empty((M, N), dtype=torch.bfloat16)
     else:
         _need(y, torch.bfloat16, "y", 2)
         _shape(y, (M, N), "y")
     need = lora_linear_mxfp4_workspace_size(M, K, N, R)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+        workspace = xq.new_empty(need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _same_device(xq, x, xsf, wq, wsf, A_cat, B_cat, y, workspace)
     if M == 0:
         return y
-    st = _launch(xq.device, lib.lg_lora_linear_mxfp4, _ptr(x), _ptr(xq), _ptr(xsf), _ptr(wq), _ptr(wsf), _ptr(A_cat),
-                 _ptr(B_cat), _ptr(y), M, K, N, R, _ptr(workspace), ws_bytes)
+    st = _launch(xq.device, lib.lg_lora_linear_mxfp4, _addr(x), _addr(xq), _addr(xsf), _addr(wq), _addr(wsf), _addr(A_cat),
+                 _addr(B_cat), _addr(y), M, K, N, R, _addr(workspace), ws_bytes)
     _check(st, "lg_lora_linear_mxfp4")
     return y
 
@@ -603,10 +609,6 @@ def _modulation(t, S, D, name):
     if t is not None:
         _need(t, torch.float32, name, 2)
         _shape(t, (S, D), name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6, post="rms", pre="rms",
@@ -643,7 +645,7 @@ def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6
     elif h_out is not None:
         raise ValueError("h_out needs b: without a block's output the stream stays as it is")
     if pre is not None and n is None:
-        n = torch.empty((M, D), dtype=torch.bfloat16, device=dev)
+        n = h.new_empty((M, D), dtype=torch.bfloat16)
     elif n is not None:
         _need(n, torch.bfloat16, "n", 2)
         _shape(n, (M, D), "n")
@@ -652,8 +654,8 @@ def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6
         width = D if quant == "mxfp8" else D // 2
         nscales = mx_scale_bytes(M, D)
         if q is None:
-            q = (torch.empty((M, width), dtype=torch.uint8, device=dev),
-                 torch.empty(nscales, dtype=torch.uint8, device=dev))
+            q = (h.new_empty((M, width), dtype=torch.uint8),
+                 h.new_empty(nscales, dtype=torch.uint8))
         codes, scales = q
         _need(codes, torch.uint8, "codes", 2)
         _shape(codes, (M, width), "codes")
@@ -708,22 +710,22 @@ def block_norm_backward(dn, dh_out, h_out, b=None, gate=None, scale=None, alpha=
         else:
             _need(db, torch.bfloat16, "db", 2)
             _shape(db, (M, D), "db")
-        dgate = torch.empty((S, D), dtype=torch.float32, device=dev)
+        dgate = h_out.new_empty((S, D), dtype=torch.float32)
     elif db is not None:
         raise ValueError("db needs b")
     if dn is not None:
-        dscale = torch.empty((S, D), dtype=torch.float32, device=dev)
-        dshift = torch.empty((S, D), dtype=torch.float32, device=dev)
+        dscale = h_out.new_empty((S, D), dtype=torch.float32)
+        dshift = h_out.new_empty((S, D), dtype=torch.float32)
     need = block_norm_backward_workspace_size(M, D, seg)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = h_out.new_empty(need, dtype=torch.uint8)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _same_device(h_out, dn, dh_out, b, gate, scale, dh, db, workspace)
     if M > 0:
         args = BlockNormBackwardArgs(_addr(dn), _addr(dh_out), _addr(h_out), _addr(b), _addr(gate), _addr(scale),
                                      _addr(dh), _addr(db), _addr(dgate), _addr(dscale), _addr(dshift), M, seg, D,
                                      _STREAM[h_out.dtype], _NORM[post], _NORM[pre], float(alpha), float(eps))
-        _check(_launch(dev, lib.lg_block_norm_backward, ctypes.byref(args), _ptr(workspace), ws_bytes),
+        _check(_launch(dev, lib.lg_block_norm_backward, ctypes.byref(args), _addr(workspace), ws_bytes),
                "lg_block_norm_backward")
     return dh, db, dgate, dscale, dshift
 

@@ -552,6 +552,25 @@ bool current_context_id(unsigned long long* id) {
   return get_id(ctx, id) == CUDA_SUCCESS;
 }
 
+cudaError_t allow_shared_memory(const void* kernel, int bytes) {
+  static std::mutex mu;
+  struct Entry {
+    const void* kernel;
+    unsigned long long context;
+  };
+  static Entry done[64];
+  static int n = 0;
+  unsigned long long ctx = 0;
+  const bool have = current_context_id(&ctx);
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; have && i < n && i < 64; ++i)
+    if (done[i].kernel == kernel && done[i].context == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // The table forgets its oldest entries; asking again is only slower.
+  if (e == cudaSuccess && have) done[n++ % 64] = Entry{kernel, ctx};
+  return e;
+}
+
 }  // namespace lg
 
 extern "C" {

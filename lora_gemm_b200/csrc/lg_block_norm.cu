@@ -709,11 +709,7 @@ cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
   if (stages > a.chunk_rows) stages = (int)a.chunk_rows;
   a.stages = stages;
   const size_t smem = stage * stages;
-  // A kernel asks for more than 48 KB first.  Always the same amount: calls
-  // from several host threads cannot lower each other's; a context keeps it,
-  // and asking again costs well under a launch.
-  const cudaError_t e = cudaFuncSetAttribute((const void*)k_block_norm_backward<FP32, CH, LAYER>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBackSmem);
+  const cudaError_t e = allow_shared_memory((const void*)k_block_norm_backward<FP32, CH, LAYER>, (int)kBackSmem);
   if (e != cudaSuccess) return e;
   k_block_norm_backward<FP32, CH, LAYER><<<(unsigned)chunks, T, smem, s>>>(a);
   return cudaGetLastError();

@@ -162,6 +162,11 @@ cudaError_t launch_lora_linear_tiles(const LinearLaunch& p, uint16_t* h, int* ke
 // and recreated (cudaDeviceReset) or a different context made current.
 bool current_context_id(unsigned long long* id);
 
+// Lets `kernel` use up to `bytes` of dynamic shared memory in the current
+// context; asks the runtime once per context and kernel.  `bytes` is the same in
+// every call for a kernel.
+cudaError_t allow_shared_memory(const void* kernel, int bytes);
+
 // Every check lg_lora_linear makes on its arguments except those on the
 // workspace, then (for M > 0) the current device's compute capability, in
 // the same order and with the same status codes; launches nothing.  Returns

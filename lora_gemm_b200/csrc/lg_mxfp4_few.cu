@@ -7,7 +7,7 @@
 // operand and the tokens the narrow one, and K is split:
 //
 //   k_few_down  h = x A_cat^T: a cluster of eight CTAs per 16 ranks, K spread
-//               over its 32 warps (mma.sync straight from registers: the FP32
+//               over its warps (mma.sync straight from registers: the FP32
 //               factors are rounded on the way, which no tensor-memory operand
 //               path does), partial sums joined through distributed shared
 //               memory.
@@ -30,7 +30,6 @@ namespace lg {
 
 namespace {
 
-constexpr int kDownWarps = 4;
 constexpr int kDownCluster = 8;
 constexpr int kDownRows = 16;  // ranks per cluster
 
@@ -77,16 +76,26 @@ struct DownArgs {
   int M, K, R;
 };
 
-// h[m, r0 .. r0 + 15]: cluster blockIdx.x / 8, its 32 warps take every 32nd
+// NG groups of eight tokens.  Eight warps per CTA split K 64 ways, so that up to
+// K = 8192 a warp issues all its loads in one batch; from 65 tokens on four
+// (their sums still fit 48 KB).
+template <int NG>
+struct DownCfg {
+  static constexpr int kWarps = NG <= 8 ? 8 : 4;
+  static constexpr int kBatch = NG <= 2 ? 4 : 2;  // steps whose loads are in flight together
+};
+
+// h[m, r0 .. r0 + 15]: cluster blockIdx.x / 8; its warps take every 64th (32nd)
 // step of 32 K.
 template <int NG>
-__global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarps * 32) k_few_down(const DownArgs a) {
-  __shared__ float sums[kDownWarps][NG * 8][kDownRows];
+__global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(DownCfg<NG>::kWarps * 32, 2)
+    k_few_down(const DownArgs a) {
+  constexpr int W = DownCfg<NG>::kWarps, U = DownCfg<NG>::kBatch;
+  __shared__ float sums[W][NG * 8][kDownRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t rank;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t rank = cluster_ctarank();
   const int r0 = (int)(blockIdx.x / kDownCluster) * kDownRows;
   const int steps = a.K / 32;
   float acc[NG][4];
@@ -97,20 +106,37 @@ __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarp
   }
   const float* pa = a.A + (int64_t)(r0 + g) * a.K + t * 8;
   const uint16_t* px = a.x + (int64_t)g * a.K + t * 8;
-#pragma unroll 4
-  for (int s = (int)rank * kDownWarps + warp; s < steps; s += kDownCluster * kDownWarps) {
-    uint32_t w[2][4];
+  for (int s0 = (int)rank * W + warp; s0 < steps; s0 += U * kDownCluster * W) {
+    float4 w[U][2][2];
+    uint4 x[U][NG];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* p = pa + (int64_t)i * 8 * a.K + s * 32;
-      round8(ld_stream4(p), ld_stream4(p + 4), w[i]);
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u * kDownCluster * W;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[u][i][0] = w[u][i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < steps) {
+          const float* p = pa + (int64_t)i * 8 * a.K + s * 32;
+          w[u][i][0] = ld_stream4(p);
+          w[u][i][1] = ld_stream4(p + 4);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        x[u][n] = make_uint4(0, 0, 0, 0);
+        if (s < steps && n * 8 + g < a.M) x[u][n] = __ldg(reinterpret_cast<const uint4*>(px + (int64_t)n * 8 * a.K + s * 32));
+      }
     }
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (n * 8 + g < a.M) x = __ldg(reinterpret_cast<const uint4*>(px + (int64_t)n * 8 * a.K + s * 32));
-      mma_bf16(acc[n], w[0][0], w[1][0], w[0][1], w[1][1], x.x, x.y);
-      mma_bf16(acc[n], w[0][2], w[1][2], w[0][3], w[1][3], x.z, x.w);
+    for (int u = 0; u < U; ++u) {
+      uint32_t v[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) round8(w[u][i][0], w[u][i][1], v[i]);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        mma_bf16(acc[n], v[0][0], v[1][0], v[0][1], v[1][1], x[u][n].x, x[u][n].y);
+        mma_bf16(acc[n], v[0][2], v[1][2], v[0][3], v[1][3], x[u][n].z, x[u][n].w);
+      }
     }
   }
 #pragma unroll
@@ -118,27 +144,26 @@ __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarp
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[warp][n * 8 + 2 * t + (e & 1)][8 * (e >> 1) + g] = acc[n][e];
   }
+  __syncthreads();
+  // The CTA's own sum, warp by warp, then the cluster's, CTA by CTA.
+  for (int i = threadIdx.x; i < a.M * kDownRows; i += W * 32) {
+    float* p = &sums[0][0][0] + i;
+    float v = p[0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) v += p[k * NG * 8 * kDownRows];
+    p[0] = v;
+  }
   cluster_barrier();
-  // Each CTA joins an eighth of the cluster's M x 16 sums, CTA by CTA and warp
-  // by warp.
-  for (int i = (int)rank * kDownWarps * 32 + threadIdx.x; i < a.M * kDownRows; i += kDownCluster * kDownWarps * 32) {
-    const int m = i / kDownRows, r = i % kDownRows;
+  for (int i = (int)rank * W * 32 + threadIdx.x; i < a.M * kDownRows; i += kDownCluster * W * 32) {
+    const uint32_t at = smem_u32(&sums[0][0][0] + i);
     float v = 0.f;
 #pragma unroll
     for (int c = 0; c < kDownCluster; ++c) {
-      uint32_t peer;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_u32(&sums[0][m][r])), "r"(c));
-#pragma unroll
-      for (int w = 0; w < kDownWarps; ++w) {
-        float p;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(p)
-                     : "r"(peer + (uint32_t)(w * NG * 8 * kDownRows * 4))
-                     : "memory");
-        v += p;
-      }
+      float p;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, (uint32_t)c)) : "memory");
+      v += p;
     }
-    a.h[(int64_t)m * a.R + r0 + r] = v;
+    a.h[(int64_t)(i / kDownRows) * a.R + r0 + i % kDownRows] = v;
   }
   // No CTA leaves while a peer may still read its sums.
   cluster_barrier();
@@ -390,8 +415,7 @@ cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h,
   a.h_stages = p.R / 32;
   a.wait_limit_ns = p.wait_limit_ns;
   constexpr int smem = (int)(1024 + C::kRing + sizeof(UpControl));
-  // A constant, so that calls from several host threads cannot lower it.
-  cudaError_t e = cudaFuncSetAttribute((const void*)k_few_up<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared_memory((const void*)k_few_up<NT>, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (p.N + kUpRows - 1) / kUpRows;
   const int split = up_split(tiles, a.q_stages + a.h_stages, p.sm_count);
@@ -415,7 +439,7 @@ cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h,
 template <int NG>
 cudaError_t down_launch(const LinearLaunch& p, const float* A_cat, float* h, cudaStream_t s) {
   const DownArgs d{reinterpret_cast<const uint16_t*>(p.x), A_cat, h, (int)p.M, p.K, p.R};
-  k_few_down<NG><<<p.R / kDownRows * kDownCluster, kDownWarps * 32, 0, s>>>(d);
+  k_few_down<NG><<<p.R / kDownRows * kDownCluster, DownCfg<NG>::kWarps * 32, 0, s>>>(d);
   return cudaGetLastError();
 }
 

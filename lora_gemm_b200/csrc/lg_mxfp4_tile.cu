@@ -446,9 +446,7 @@ cudaError_t tile_launch(const Product& p, int pairs, uint64_t wait_limit_ns, cud
   a.y_off = (uint32_t)a.stages * C::STAGE;
   a.control_off = a.y_off + Y_BYTES;
   a.wait_limit_ns = wait_limit_ns;
-  // A constant: asked anew on every launch, so a new context has it too.
-  cudaError_t e = cudaFuncSetAttribute((const void*)k_mxfp4_tile<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)MAX_SMEM);
+  cudaError_t e = allow_shared_memory((const void*)k_mxfp4_tile<TN>, (int)MAX_SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (a.tiles < pairs ? a.tiles : pairs)), 1, 1);
