@@ -67,6 +67,52 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Two FP32 values in a register pair, for the instructions that work on both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// Eight bf16 values as four pairs.
+__device__ __forceinline__ void unpack8(uint4 q, F2 (&v)[4]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = split(v[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Raw bits of eight stream values: 16 bytes (bf16) or 32 (FP32).
 template <bool FP32>
 struct Raw8 {
@@ -93,7 +139,32 @@ struct Raw8 {
       unpack8(q[0], v);
     }
   }
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+    if constexpr (FP32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[2 * i] = f2(__uint_as_float(q[i].x), __uint_as_float(q[i].y));
+        v[2 * i + 1] = f2(__uint_as_float(q[i].z), __uint_as_float(q[i].w));
+      }
+    } else {
+      unpack8(q[0], v);
+    }
+  }
 };
+template <bool FP32>
+__device__ __forceinline__ void store_stream8(void* base, int64_t at, const F2 (&v)[4]) {
+  if constexpr (FP32) {
+    float* p = reinterpret_cast<float*>(base) + at;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = split(v[2 * i]), b = split(v[2 * i + 1]);
+      st_stream(p + 4 * i, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                                      __float_as_uint(b.y)));
+    }
+  } else {
+    st_stream(reinterpret_cast<uint16_t*>(base) + at, pack8(v));
+  }
+}
 // Stores eight values in the stream's type; v becomes what was stored.
 template <bool FP32>
 __device__ __forceinline__ void store_stream8(void* base, int64_t at, float (&v)[8]) {
@@ -118,6 +189,17 @@ __device__ __forceinline__ void load_mod8(const float* base, int64_t at, float o
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = other;
+  }
+}
+
+__device__ __forceinline__ void load_mod8(const float* base, int64_t at, float other, F2 (&v)[4]) {
+  if (base) {
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(base + at));
+    const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(base + at + 4));
+    v[0].v = a.x, v[1].v = a.y, v[2].v = b.x, v[3].v = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(other, other);
   }
 }
 
@@ -430,13 +512,13 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
     cp_async_commit();  // a group per row, empty past the last one
   };
 
-  float acc[3][CH][8];
+  F2 acc[3][CH][4];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[k][c][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[k][c][i] = f2(0.f, 0.f);
     }
   }
   // Pieces of absent inputs and of columns past D read as zero.
@@ -469,28 +551,34 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
 
     float mx = 0.f, mu = 0.f;
     if constexpr (LAYER) {
-      float m[8] = {};
+      F2 sx = f2(0.f, 0.f), su = sx;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float x[8], u[8];
+        F2 x[4], u[4];
         rx8[c].get(x);
         unpack8(rb8[c], u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          m[0] += x[i];
-          m[1] += u[i];
+        for (int i = 0; i < 4; ++i) {
+          sx = sx + x[i];
+          su = su + u[i];
         }
       }
+      float m[8] = {};
+      m[0] = split(sx).x + split(sx).y;
+      m[1] = split(su).x + split(su).y;
       cta_sums<8>(m, warps, mean_slots[buf]);
       if (a.pre == kLayer) mx = m[0] * inv_d;
       if (a.post == kLayer) mu = m[1] * inv_d;
     }
-    float q[N] = {};
+    const F2 nmx = f2(-mx, -mx), nmu = f2(-mu, -mu);
+    F2 p[LAYER ? 12 : 6];
+#pragma unroll
+    for (int k = 0; k < (LAYER ? 12 : 6); ++k) p[k] = f2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (!live[c]) continue;
       const int col = (c * T + t) * 8;
-      float x[8], d[8], g[8], u[8], sc[8], gt[8];
+      F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
       rx8[c].get(x);
       rd8[c].get(d);
       unpack8(rn8[c], g);
@@ -498,27 +586,35 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
       load_mod8(scale, col, 0.f, sc);
       load_mod8(gate, col, 1.f, gt);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[2][c][i] += g[i];
-        const float w = g[i] * (1.0f + sc[i]);
-        x[i] -= mx;
-        u[i] -= mu;
-        const float tb = gt[i] * u[i];
-        q[0] = fmaf(x[i], x[i], q[0]);
-        q[1] = fmaf(u[i], u[i], q[1]);
-        q[2] = fmaf(w, x[i], q[2]);
-        q[3] = fmaf(tb, d[i], q[3]);
-        q[4] = fmaf(tb, w, q[4]);
-        q[5] = fmaf(tb, x[i], q[5]);
+      for (int i = 0; i < 4; ++i) {
+        acc[2][c][i] = acc[2][c][i] + g[i];
+        const F2 w = fma(g[i], sc[i], g[i]);
         if constexpr (LAYER) {
-          q[6] += w;
-          q[7] += tb;
-          q[8] = fmaf(gt[i], d[i], q[8]);
-          q[9] = fmaf(gt[i], w, q[9]);
-          q[10] += gt[i];
-          q[11] = fmaf(gt[i], x[i], q[11]);
+          x[i] = x[i] + nmx;
+          u[i] = u[i] + nmu;
+        }
+        const F2 tb = gt[i] * u[i];
+        p[0] = fma(x[i], x[i], p[0]);
+        p[1] = fma(u[i], u[i], p[1]);
+        p[2] = fma(w, x[i], p[2]);
+        p[3] = fma(tb, d[i], p[3]);
+        p[4] = fma(tb, w, p[4]);
+        p[5] = fma(tb, x[i], p[5]);
+        if constexpr (LAYER) {
+          p[6] = p[6] + w;
+          p[7] = p[7] + tb;
+          p[8] = fma(gt[i], d[i], p[8]);
+          p[9] = fma(gt[i], w, p[9]);
+          p[10] = p[10] + gt[i];
+          p[11] = fma(gt[i], x[i], p[11]);
         }
       }
+    }
+    float q[N] = {};
+#pragma unroll
+    for (int k = 0; k < (LAYER ? 12 : 6); ++k) {
+      const float2 h = split(p[k]);
+      q[k] = h.x + h.y;
     }
     cta_sums<N>(q, warps, slots[buf]);
     const float rx = a.dn ? 1.0f / sqrtf(q[0] * inv_d + a.eps) : 0.f;
@@ -531,11 +627,13 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
       if (a.post == kLayer) mw = inv_d * (q[8] + rx * (q[9] - mg * q[10]) - k * q[11]);
     }
     const float mwu = a.post == kNone ? 0.f : ru * swu * inv_d;  // mean of w u
+    const F2 rx2 = f2(rx, rx), nk2 = f2(-k, -k), ru2 = f2(ru, ru), nmg2 = f2(-rx * mg, -rx * mg);
+    const F2 alpha2 = f2(a.alpha, a.alpha), nmw2 = f2(-ru * mw, -ru * mw), nmwu2 = f2(-ru * mwu, -ru * mwu);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (!live[c]) continue;
       const int col = (c * T + t) * 8;
-      float x[8], d[8], g[8], u[8], sc[8], gt[8];
+      F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
       rx8[c].get(x);
       rd8[c].get(d);
       unpack8(rn8[c], g);
@@ -543,14 +641,22 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
       load_mod8(scale, col, 0.f, sc);
       load_mod8(gate, col, 1.f, gt);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] -= mx;
-        u[i] = (u[i] - mu) * ru;
-        acc[1][c][i] = fmaf(g[i], x[i] * rx, acc[1][c][i]);
-        d[i] = fmaf(rx, g[i] * (1.0f + sc[i]) - mg, d[i]) - k * x[i];
-        acc[0][c][i] = fmaf(d[i], u[i], acc[0][c][i]);
-        u[i] = ru * (gt[i] * d[i] - mw - u[i] * mwu);
-        d[i] *= a.alpha;
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (LAYER) {
+          x[i] = x[i] + nmx;
+          u[i] = u[i] + nmu;
+        }
+        u[i] = u[i] * ru2;
+        const F2 rg = rx2 * g[i];
+        acc[1][c][i] = fma(rg, x[i], acc[1][c][i]);
+        d[i] = fma(rg, sc[i], rg + d[i]);
+        if constexpr (LAYER) d[i] = d[i] + nmg2;
+        d[i] = fma(nk2, x[i], d[i]);
+        acc[0][c][i] = fma(d[i], u[i], acc[0][c][i]);
+        const F2 w = (ru2 * gt[i]) * d[i];
+        u[i] = fma(nmwu2, u[i], w);
+        if constexpr (LAYER) u[i] = u[i] + nmw2;
+        d[i] = d[i] * alpha2;
       }
       const int64_t at = row * a.D + col;
       if (a.dh) store_stream8<FP32>(a.dh, at, d);
@@ -565,8 +671,11 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
     for (int c = 0; c < CH; ++c) {
       if (!live[c]) continue;
       float4* o = reinterpret_cast<float4*>(a.sums[k] + blockIdx.x * a.sum_stride + (c * T + t) * 8);
-      o[0] = make_float4(acc[k][c][0], acc[k][c][1], acc[k][c][2], acc[k][c][3]);
-      o[1] = make_float4(acc[k][c][4], acc[k][c][5], acc[k][c][6], acc[k][c][7]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = split(acc[k][c][2 * i]), y = split(acc[k][c][2 * i + 1]);
+        o[i] = make_float4(x.x, x.y, y.x, y.y);
+      }
     }
   }
 }
