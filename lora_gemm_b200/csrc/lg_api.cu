@@ -197,7 +197,7 @@ lg_status lg_mxfp4_quantize(const void* in, int64_t rows, int K, void* codes, vo
   if (st != LG_OK) return st;
   return launched(lg::launch_mxfp4_quantize(reinterpret_cast<const uint16_t*>(in), rows, K,
                                             reinterpret_cast<uint8_t*>(codes), reinterpret_cast<uint8_t*>(scales),
-                                            sms, as_stream(stream)),
+                                            as_stream(stream)),
                   1);
 }
 
@@ -214,7 +214,7 @@ lg_status lg_mxfp4_dequantize(const void* codes, const void* scales, int64_t row
   if (st != LG_OK) return st;
   return launched(lg::launch_mxfp4_dequantize(reinterpret_cast<const uint8_t*>(codes),
                                               reinterpret_cast<const uint8_t*>(scales), rows, K,
-                                              reinterpret_cast<uint16_t*>(out), sms, as_stream(stream)),
+                                              reinterpret_cast<uint16_t*>(out), as_stream(stream)),
                   1);
 }
 

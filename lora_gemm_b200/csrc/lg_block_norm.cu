@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       uint32_t sb;
       if (a.format == kCodesMxfp4) {
-        sb = mxfp4_scale_byte(mx_block_max(mx_abs_max8(w)));
+        sb = mxfp4_scale_byte(mx_block_max(w));
         if (live[c]) *reinterpret_cast<uint32_t*>(a.codes + (at + col) / 2) = mxfp4_codes8(w, sb);
       } else {
         float m = 0.f;

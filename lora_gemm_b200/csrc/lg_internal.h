@@ -49,9 +49,9 @@ cudaError_t launch_mx_quantize(const uint16_t* in, int64_t rows, int K, uint8_t*
 // MXFP4 quantization of bf16 rows [rows, K] along K (K % 128 == 0): packed
 // E2M1 codes [rows, K / 2] and E8M0 scales in the blocked layout; and back.
 cudaError_t launch_mxfp4_quantize(const uint16_t* in, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
-                                  int sm_count, cudaStream_t s);
+                                  cudaStream_t s);
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, uint16_t* out,
-                                    int sm_count, cudaStream_t s);
+                                    cudaStream_t s);
 
 // Block norms; fields as in lg_block_norm_args / lg_block_norm_backward_args.
 struct BlockNormLaunch {

@@ -17,20 +17,16 @@ __device__ __forceinline__ int64_t mx_scale_offset(int64_t row, int block, int k
   return (((row >> 7) * k_groups + (block >> 2)) << 9) + 16 * (r & 31) + 4 * (r >> 5) + (block & 3);
 }
 
-// Bits of the largest magnitude among eight bf16 values (packed pairs), as an
-// FP32 word.  An integer maximum of the magnitudes: NaN and infinity, whose
-// exponent field is all ones, stay on top.
-__device__ __forceinline__ uint32_t mx_abs_max8(const uint32_t (&w)[4]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
-  return m;
-}
-
-// The block's maximum over the four lanes that share it.
-__device__ __forceinline__ uint32_t mx_block_max(uint32_t m) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+// The largest magnitude among a block's bf16 values as an FP32 word: eight
+// packed values of this lane and those of the three lanes beside it.  An
+// unsigned maximum of the magnitudes' bits, two at a time: NaN and infinity,
+// whose exponent field is all ones, stay on top.
+__device__ __forceinline__ uint32_t mx_block_max(const uint32_t (&w)[4]) {
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                        __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 // 2^-e as an FP32 number, e in [-127, 127] (2^-127 is subnormal).
@@ -52,12 +48,21 @@ __device__ __forceinline__ uint32_t mxfp4_scale_byte(uint32_t amax) {
 __device__ __forceinline__ uint32_t mxfp4_codes8(const uint32_t (&w)[4], uint32_t sb) {
   if (sb == 255u) return 0u;
   const float inv = mx_inverse_scale((int)sb - 127);
-  uint32_t out = 0;
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
-    out |= (uint32_t)__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest) << (8 * i);
+    v[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
   }
+  uint32_t out;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(out)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return out;
 }
 
