@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kNone = 0, kLayer = 2;  // LG_NORM_NONE, LG_NORM_LAYER (LG_NORM_RMS needs no test)
 constexpr int kCodesMxfp4 = 2;  // LG_CODES_MXFP4; any other nonzero format is MXFP8
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 64;  // of a row: eight CTAs of at most eight warps, four of 14, two of 14, one of 16
 
 // Eight consecutive values of a row as FP32; loads and stores of the stream
 // data do not allocate in L1.
@@ -189,17 +189,6 @@ __device__ __forceinline__ void load_mod8(const float* base, int64_t at, float o
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = other;
-  }
-}
-
-__device__ __forceinline__ void load_mod8(const float* base, int64_t at, float other, F2 (&v)[4]) {
-  if (base) {
-    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(base + at));
-    const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(base + at + 4));
-    v[0].v = a.x, v[1].v = a.y, v[2].v = b.x, v[3].v = b.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f2(other, other);
   }
 }
 
@@ -374,7 +363,8 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
 // Backward.
 // ---------------------------------------------------------------------------
 constexpr int kBackStagesMax = 4;
-constexpr size_t kBackSmem = 200 * 1024;  // for the row stages, of the 227 KB a CTA may have
+constexpr int kBackThreads = 448;              // at most, of eight columns each
+constexpr size_t kBackSmem = 106 * 1024;  // modulation and row stages: two CTAs per SM
 
 struct BackArgs {
   const void* dn;
@@ -409,13 +399,21 @@ __device__ __forceinline__ void cp_async_wait(int n) {
   else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// Sums of N = 8 or 16 values over all threads of the CTA, in every thread.
-// Within a warp each step exchanges half of the values a lane still holds with
-// the lane whose bit differs (9 shuffles for 8 values instead of 40): value i
-// ends in lanes i * 32 / N and up.  `slot` [N][kMaxWarps] is not written again
-// before the CTA's next but one call.
-template <int N>
-__device__ __forceinline__ void cta_sums(float (&v)[N], int warps, float (*slot)[kMaxWarps]) {
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of N = 8 or 16 values over all threads of the SPLIT CTAs that share a
+// row, in every thread.  Within a warp each step exchanges half of the values a
+// lane still holds with the lane whose bit differs (9 shuffles for 8 values
+// instead of 40): value i ends in lanes i * 32 / N and up.  Every warp leaves its
+// sums in all SPLIT CTAs' `slot`, at the same place, so that all
+// add them up in the same order; `slot` is not written again before the next
+// but one call.  (Its rows are 32 / N words longer than the warps need: the
+// lanes' reads then fall into different banks.)
+template <int N, int SPLIT>
+__device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_t rank,
+                                               float (*slot)[kMaxWarps + 32 / N]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int half = N / 2;
 #pragma unroll
@@ -437,12 +435,28 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], int warps, float (*slot)
   }
   constexpr int kLanes = 32 / N;  // lanes that share a value
   float total = v[0];
-  if (warps > 1) {
+  const int all = SPLIT * warps;
+  if (all > 1) {
     const int idx = lane / kLanes, sub = lane % kLanes;
-    if (sub == 0) slot[idx][warp] = total;
-    __syncthreads();
+    float* mine = &slot[idx][(int)rank * warps + warp];
+    if constexpr (SPLIT == 1) {
+      if (sub == 0) *mine = total;
+      __syncthreads();
+    } else {
+      if (sub == 0) {
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine);
+#pragma unroll
+        for (uint32_t c = 0; c < SPLIT; ++c) {
+          uint32_t peer;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(c));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer), "f"(total) : "memory");
+        }
+      }
+      cluster_barrier();
+    }
     total = 0.f;
-    for (int w = sub; w < warps; w += kLanes) total += slot[idx][w];
+#pragma unroll 4
+    for (int w = sub; w < all; w += kLanes) total += slot[idx][w];
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
@@ -450,11 +464,16 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], int warps, float (*slot)
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, total, i * kLanes);
 }
 
-// One CTA: consecutive rows of one segment; thread t always has columns
-// [8 (c T + t), + 8).  Rows arrive through a ring of shared-memory stages
-// filled by cp.async: every thread copies and reads its own 16-byte pieces, so
-// the ring needs no barrier, and the rows in flight cost no registers (which
-// hold the three column sums).
+// A cluster of SPLIT CTAs: consecutive rows of one segment; every thread always
+// has the same eight columns.  A row of 7168 is two CTAs of 448 threads rather
+// than one of 896: the three column sums fill the registers of an SM either way
+// (one CTA of 896 threads, or two of 448), but two CTAs of different clusters are
+// at different points of their rows, and one works while the other waits for its
+// row's sums.  Rows arrive through a ring of shared-memory stages filled by
+// cp.async: every thread copies and reads its own 16-byte pieces, so the ring
+// needs no barrier, and the rows in flight cost no registers.  Gate and scale
+// are laid out in shared memory by thread (read in place, a thread's eight FP32
+// values are 32 bytes from its neighbour's and every load takes twice the passes).
 //
 // All row sums come from one pass (two with a layer norm, whose means are
 // taken first so that the squares are those of centred values).  With x, b the
@@ -465,108 +484,104 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], int warps, float (*slot)
 //   sum w   =     sum t dh_out   + rx (sum t g   - mean g sum t)   - k sum t x
 //   db = ru (w - mean w - u mean(w u))
 // so the second norm's sums need no second pass over the first one's result.
-template <bool FP32, int CH, bool LAYER>
-__global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward(const BackArgs a) {
+template <bool FP32, int SPLIT, bool LAYER>
+__global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const BackArgs a) {
   constexpr int N = LAYER ? 16 : 8;
   constexpr int W = FP32 ? 2 : 1;              // 16-byte pieces of eight stream values
   constexpr int PIECES = 2 * W + 2;            // h, dh_out, dn, b
-  extern __shared__ uint4 ring[];              // [stages][CH][PIECES][T]
-  __shared__ float slots[2][N][kMaxWarps];
-  __shared__ float mean_slots[2][8][kMaxWarps];
+  extern __shared__ uint4 shared[];            // [4][T] gate and scale, then [stages][PIECES][T]
+  __shared__ float slots[2][N][kMaxWarps + 32 / N];
+  __shared__ float mean_slots[2][8][kMaxWarps + 4];
   const int T = (int)blockDim.x, warps = T >> 5, t = (int)threadIdx.x;
-  int64_t s = blockIdx.x / a.seg_chunks;
+  uint32_t rank = 0;
+  if constexpr (SPLIT > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int64_t chunk = blockIdx.x / SPLIT;
+  int64_t s = chunk / a.seg_chunks;
   if (s >= a.segments) s = a.segments - 1;
-  const int64_t first = s * a.seg + (blockIdx.x - s * a.seg_chunks) * a.chunk_rows;
+  const int64_t first = s * a.seg + (chunk - s * a.seg_chunks) * a.chunk_rows;
   int64_t last = first + a.chunk_rows;
   if (last > (s + 1) * a.seg) last = (s + 1) * a.seg;
   if (last > a.M) last = a.M;
   const float inv_d = 1.0f / (float)a.D;
-  const float* gate = a.gate ? a.gate + s * a.D : nullptr;
-  const float* scale = a.scale ? a.scale + s * a.D : nullptr;
-  bool live[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) live[c] = (c * T + t) * 8 < a.D;
+  const int col = ((int)rank * T + t) * 8;
+  const bool live = col < a.D;
 
-  auto piece = [&](int stage, int c, int k) { return &ring[((stage * CH + c) * PIECES + k) * T + t]; };
+  uint4* ring = shared + 4 * T;
+  auto piece = [&](int stage, int k) { return &ring[(stage * PIECES + k) * T + t]; };
   auto fetch = [&](int64_t row, int stage) {
-    if (row < last) {
+    if (row < last && live) {
+      const int64_t at = row * a.D + col;
+      if (a.dn) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (!live[c]) continue;
-        const int64_t at = row * a.D + (c * T + t) * 8;
-        if (a.dn) {
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-            cp_async16(smem_addr(piece(stage, c, w)), reinterpret_cast<const uint8_t*>(a.h) + at * (2 * W) + 16 * w);
-          cp_async16(smem_addr(piece(stage, c, 2 * W)), reinterpret_cast<const uint8_t*>(a.dn) + at * 2);
-        }
-        if (a.dh_out) {
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-            cp_async16(smem_addr(piece(stage, c, W + w)),
-                       reinterpret_cast<const uint8_t*>(a.dh_out) + at * (2 * W) + 16 * w);
-        }
-        if (a.b) cp_async16(smem_addr(piece(stage, c, 2 * W + 1)), reinterpret_cast<const uint8_t*>(a.b) + at * 2);
+        for (int w = 0; w < W; ++w)
+          cp_async16(smem_addr(piece(stage, w)), reinterpret_cast<const uint8_t*>(a.h) + at * (2 * W) + 16 * w);
+        cp_async16(smem_addr(piece(stage, 2 * W)), reinterpret_cast<const uint8_t*>(a.dn) + at * 2);
       }
+      if (a.dh_out) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          cp_async16(smem_addr(piece(stage, W + w)), reinterpret_cast<const uint8_t*>(a.dh_out) + at * (2 * W) + 16 * w);
+      }
+      if (a.b) cp_async16(smem_addr(piece(stage, 2 * W + 1)), reinterpret_cast<const uint8_t*>(a.b) + at * 2);
     }
     cp_async_commit();  // a group per row, empty past the last one
   };
 
-  F2 acc[3][CH][4];
+  F2 acc[3][4];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[k][c][i] = f2(0.f, 0.f);
-    }
+    for (int i = 0; i < 4; ++i) acc[k][i] = f2(0.f, 0.f);
   }
   // Pieces of absent inputs and of columns past D read as zero.
   for (int st = 0; st < a.stages; ++st) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) *piece(st, c, k) = make_uint4(0, 0, 0, 0);
-    }
+    for (int k = 0; k < PIECES; ++k) *piece(st, k) = make_uint4(0, 0, 0, 0);
   }
   for (int st = 0; st < a.stages; ++st) fetch(first + st, st);
+  // Gate in pieces 0 and 1 of this thread, scale in 2 and 3.
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float* m = k < 2 ? a.gate : a.scale;
+    float4 v = k < 2 ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m && live) v = __ldg(reinterpret_cast<const float4*>(m + s * a.D + col + 4 * (k & 1)));
+    if (!live) v = make_float4(0.f, 0.f, 0.f, 0.f);
+    reinterpret_cast<float4*>(shared)[k * T + t] = v;
+  }
+  auto mod = [&](int k, F2 (&v)[4]) {
+    const ulonglong2 x = reinterpret_cast<const ulonglong2*>(shared)[k * T + t];
+    const ulonglong2 y = reinterpret_cast<const ulonglong2*>(shared)[(k + 1) * T + t];
+    v[0].v = x.x, v[1].v = x.y, v[2].v = y.x, v[3].v = y.y;
+  };
+  if constexpr (SPLIT > 1) cluster_barrier();  // the peers' shared memory is there
 
   int buf = 0, stage = 0;
   for (int64_t row = first; row < last; ++row, buf ^= 1) {
     cp_async_wait(a.stages - 1);
-    Raw8<FP32> rx8[CH], rd8[CH];
-    uint4 rn8[CH], rb8[CH];
+    Raw8<FP32> rx8, rd8;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        rx8[c].q[w] = *piece(stage, c, w);
-        rd8[c].q[w] = *piece(stage, c, W + w);
-      }
-      rn8[c] = *piece(stage, c, 2 * W);
-      rb8[c] = *piece(stage, c, 2 * W + 1);
+    for (int w = 0; w < W; ++w) {
+      rx8.q[w] = *piece(stage, w);
+      rd8.q[w] = *piece(stage, W + w);
     }
+    const uint4 rn8 = *piece(stage, 2 * W), rb8 = *piece(stage, 2 * W + 1);
     fetch(row + a.stages, stage);
     if (++stage == a.stages) stage = 0;
 
     float mx = 0.f, mu = 0.f;
     if constexpr (LAYER) {
-      F2 sx = f2(0.f, 0.f), su = sx;
+      F2 sx = f2(0.f, 0.f), su = sx, x[4], u[4];
+      rx8.get(x);
+      unpack8(rb8, u);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        F2 x[4], u[4];
-        rx8[c].get(x);
-        unpack8(rb8[c], u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sx = sx + x[i];
-          su = su + u[i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        sx = sx + x[i];
+        su = su + u[i];
       }
       float m[8] = {};
       m[0] = split(sx).x + split(sx).y;
       m[1] = split(su).x + split(su).y;
-      cta_sums<8>(m, warps, mean_slots[buf]);
+      row_group_sums<8, SPLIT>(m, warps, rank, mean_slots[buf]);
       if (a.pre == kLayer) mx = m[0] * inv_d;
       if (a.post == kLayer) mu = m[1] * inv_d;
     }
@@ -574,20 +589,17 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
     F2 p[LAYER ? 12 : 6];
 #pragma unroll
     for (int k = 0; k < (LAYER ? 12 : 6); ++k) p[k] = f2(0.f, 0.f);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (!live[c]) continue;
-      const int col = (c * T + t) * 8;
+    if (live) {
       F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
-      rx8[c].get(x);
-      rd8[c].get(d);
-      unpack8(rn8[c], g);
-      unpack8(rb8[c], u);
-      load_mod8(scale, col, 0.f, sc);
-      load_mod8(gate, col, 1.f, gt);
+      rx8.get(x);
+      rd8.get(d);
+      unpack8(rn8, g);
+      unpack8(rb8, u);
+      mod(2, sc);
+      mod(0, gt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[2][c][i] = acc[2][c][i] + g[i];
+        acc[2][i] = acc[2][i] + g[i];
         const F2 w = fma(g[i], sc[i], g[i]);
         if constexpr (LAYER) {
           x[i] = x[i] + nmx;
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
       const float2 h = split(p[k]);
       q[k] = h.x + h.y;
     }
-    cta_sums<N>(q, warps, slots[buf]);
+    row_group_sums<N, SPLIT>(q, warps, rank, slots[buf]);
     const float rx = a.dn ? 1.0f / sqrtf(q[0] * inv_d + a.eps) : 0.f;
     const float ru = a.post == kNone ? 1.0f : 1.0f / sqrtf(q[1] * inv_d + a.eps);
     const float k = rx * rx * rx * (q[2] * inv_d);
@@ -629,17 +641,14 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
     const float mwu = a.post == kNone ? 0.f : ru * swu * inv_d;  // mean of w u
     const F2 rx2 = f2(rx, rx), nk2 = f2(-k, -k), ru2 = f2(ru, ru), nmg2 = f2(-rx * mg, -rx * mg);
     const F2 alpha2 = f2(a.alpha, a.alpha), nmw2 = f2(-ru * mw, -ru * mw), nmwu2 = f2(-ru * mwu, -ru * mwu);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (!live[c]) continue;
-      const int col = (c * T + t) * 8;
+    if (live) {
       F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
-      rx8[c].get(x);
-      rd8[c].get(d);
-      unpack8(rn8[c], g);
-      unpack8(rb8[c], u);
-      load_mod8(scale, col, 0.f, sc);
-      load_mod8(gate, col, 1.f, gt);
+      rx8.get(x);
+      rd8.get(d);
+      unpack8(rn8, g);
+      unpack8(rb8, u);
+      mod(2, sc);
+      mod(0, gt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (LAYER) {
@@ -648,11 +657,11 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
         }
         u[i] = u[i] * ru2;
         const F2 rg = rx2 * g[i];
-        acc[1][c][i] = fma(rg, x[i], acc[1][c][i]);
+        acc[1][i] = fma(rg, x[i], acc[1][i]);
         d[i] = fma(rg, sc[i], rg + d[i]);
         if constexpr (LAYER) d[i] = d[i] + nmg2;
         d[i] = fma(nk2, x[i], d[i]);
-        acc[0][c][i] = fma(d[i], u[i], acc[0][c][i]);
+        acc[0][i] = fma(d[i], u[i], acc[0][i]);
         const F2 w = (ru2 * gt[i]) * d[i];
         u[i] = fma(nmwu2, u[i], w);
         if constexpr (LAYER) u[i] = u[i] + nmw2;
@@ -664,18 +673,15 @@ __global__ void __launch_bounds__(CH == 1 ? 896 : 1024, 1) k_block_norm_backward
     }
   }
   cp_async_wait(0);
+  if (!live) return;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (!a.sums[k]) continue;
+    float4* o = reinterpret_cast<float4*>(a.sums[k] + chunk * a.sum_stride + col);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (!live[c]) continue;
-      float4* o = reinterpret_cast<float4*>(a.sums[k] + blockIdx.x * a.sum_stride + (c * T + t) * 8);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 x = split(acc[k][c][2 * i]), y = split(acc[k][c][2 * i + 1]);
-        o[i] = make_float4(x.x, x.y, y.x, y.y);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = split(acc[k][2 * i]), y = split(acc[k][2 * i + 1]);
+      o[i] = make_float4(x.x, x.y, y.x, y.y);
     }
   }
 }
@@ -745,8 +751,16 @@ cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);
 }
 
-// Threads of a backward CTA: eight columns each up to D = 7168, sixteen above.
-int back_threads(int D) { return D <= 7168 ? 32 * ((D / 8 + 31) / 32) : 32 * ((D / 8 + 63) / 64); }
+// CTAs that share a row in the backward pass, and their threads.
+int back_split(int D) {
+  int split = 1;
+  while ((D / 8 + split - 1) / split > kBackThreads) split *= 2;
+  return split;
+}
+int back_threads(int D) {
+  const int split = back_split(D);
+  return 32 * ((D / 8 + 32 * split - 1) / (32 * split));
+}
 
 // How the backward pass splits its rows: `per` chunks of `rows` rows in a full
 // segment, `total` in all.  A chunk stays within a segment.
@@ -758,11 +772,11 @@ Chunks back_chunks(int64_t M, int D, int64_t seg) {
   Chunks c;
   c.segments = (M + seg - 1) / seg;
   const int64_t rest = M - (c.segments - 1) * seg;
-  // One wave: the CTAs that 148 SMs hold at ~72 registers a thread.  A CTA's
-  // partial sums cost as much traffic as about one of its rows, and its
+  // One wave: the clusters that 148 SMs hold at 72 registers a thread.  A
+  // chunk's partial sums cost as much traffic as about one of its rows, and its
   // rows follow one another: not less than four of them.
-  const int64_t resident = 896 / back_threads(D) < 1 ? 1 : 896 / back_threads(D);
-  const int64_t target = 148 * (resident > 8 ? 8 : resident);
+  const int64_t resident = 2 * kBackThreads / back_threads(D);
+  const int64_t target = 148 * (resident > 8 ? 8 : resident) / back_split(D);
   c.rows = (M + target - 1) / target;
   if (c.rows < 4) c.rows = 4;
   if (c.rows > seg) c.rows = seg;
@@ -809,29 +823,45 @@ size_t block_norm_backward_workspace(int64_t M, int D, int64_t segment_tokens) {
 
 namespace {
 
-template <bool FP32, int CH, bool LAYER>
+template <bool FP32, int SPLIT, bool LAYER>
 cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
-  const size_t stage = (size_t)CH * (FP32 ? 6 : 4) * 16 * T;
-  int stages = (int)(kBackSmem / stage);
+  const size_t mods = (size_t)64 * T, stage = (size_t)(FP32 ? 6 : 4) * 16 * T;
+  int stages = (int)((kBackSmem - mods) / stage);
   if (stages > kBackStagesMax) stages = kBackStagesMax;
-  if (stages < 1) stages = 1;  // the widest FP32 rows: 192 KB, which still fits
   if (stages > a.chunk_rows) stages = (int)a.chunk_rows;
   a.stages = stages;
-  const size_t smem = stage * stages;
-  const cudaError_t e = allow_shared_memory((const void*)k_block_norm_backward<FP32, CH, LAYER>, (int)kBackSmem);
+  const cudaError_t e = allow_shared_memory((const void*)k_block_norm_backward<FP32, SPLIT, LAYER>, (int)kBackSmem);
   if (e != cudaSuccess) return e;
-  k_block_norm_backward<FP32, CH, LAYER><<<(unsigned)chunks, T, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(chunks * SPLIT), 1, 1);
+  cfg.blockDim = dim3((unsigned)T, 1, 1);
+  cfg.dynamicSmemBytes = mods + stage * stages;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = SPLIT;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_block_norm_backward<FP32, SPLIT, LAYER>, (const BackArgs)a);
+}
+
+template <bool FP32, int SPLIT>
+cudaError_t back_kind(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
+  const bool layer = a.pre == kLayer || a.post == kLayer;
+  return layer ? back_launch<FP32, SPLIT, true>(a, chunks, T, s) : back_launch<FP32, SPLIT, false>(a, chunks, T, s);
 }
 
 template <bool FP32>
 cudaError_t back_dispatch(BackArgs& a, int64_t chunks, cudaStream_t s) {
   const int T = back_threads(a.D);
-  const bool layer = a.pre == kLayer || a.post == kLayer;
-  if (a.D <= 7168) {
-    return layer ? back_launch<FP32, 1, true>(a, chunks, T, s) : back_launch<FP32, 1, false>(a, chunks, T, s);
+  switch (back_split(a.D)) {
+    case 1: return back_kind<FP32, 1>(a, chunks, T, s);
+    case 2: return back_kind<FP32, 2>(a, chunks, T, s);
+    case 4: return back_kind<FP32, 4>(a, chunks, T, s);
+    default: return back_kind<FP32, 8>(a, chunks, T, s);
   }
-  return layer ? back_launch<FP32, 2, true>(a, chunks, T, s) : back_launch<FP32, 2, false>(a, chunks, T, s);
 }
 
 }  // namespace
