@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kNone = 0, kLayer = 2;  // LG_NORM_NONE, LG_NORM_LAYER (LG_NORM_RMS needs no test)
 constexpr int kCodesMxfp4 = 2;  // LG_CODES_MXFP4; any other nonzero format is MXFP8
-constexpr int kMaxWarps = 64;  // of a row: eight CTAs of at most eight warps, four of 14, two of 14, one of 16
+constexpr int kMaxWarps = 32;  // of a row in one CTA
 
 // Eight consecutive values of a row as FP32; loads and stores of the stream
 // data do not allocate in L1.
@@ -260,7 +260,7 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[
     for (int i = 0; i < 8; ++i) q[0] = fmaf(v[c][i], v[c][i], q[0]);
   }
   row_sums<1>(q, warps, slot + 1);
-  const float r = 1.0f / sqrtf(q[0] / (float)D + eps);
+  const float r = rsqrtf(q[0] / (float)D + eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
@@ -409,11 +409,18 @@ __device__ __forceinline__ void cluster_barrier() {
 // instead of 40): value i ends in lanes i * 32 / N and up.  Every warp leaves its
 // sums in all SPLIT CTAs' `slot`, at the same place, so that all
 // add them up in the same order; `slot` is not written again before the next
-// but one call.  (Its rows are 32 / N words longer than the warps need: the
-// lanes' reads then fall into different banks.)
+// but one call.  (Its rows are 32 / N words longer than 64: the lanes'
+// reads then fall into different banks.)
 template <int N, int SPLIT>
-__device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_t rank,
-                                               float (*slot)[kMaxWarps + 32 / N]) {
+struct Slots {
+  static constexpr int kWarps = SPLIT * (SPLIT == 8 ? 8 : kBackThreads / 32);  // at most, of a row
+  static constexpr int kLanes = 32 / N;                                        // lanes that share a value
+  static constexpr int kReads = (kWarps + kLanes - 1) / kLanes;
+  static constexpr int kStride = 64 + kLanes;
+  float v[N][kStride];
+};
+template <int N, int SPLIT>
+__device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_t rank, Slots<N, SPLIT>& slot) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int half = N / 2;
 #pragma unroll
@@ -433,12 +440,11 @@ __device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_
       v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
     }
   }
-  constexpr int kLanes = 32 / N;  // lanes that share a value
+  constexpr int kLanes = Slots<N, SPLIT>::kLanes;
   float total = v[0];
-  const int all = SPLIT * warps;
-  if (all > 1) {
+  if (SPLIT > 1 || warps > 1) {
     const int idx = lane / kLanes, sub = lane % kLanes;
-    float* mine = &slot[idx][(int)rank * warps + warp];
+    float* mine = &slot.v[idx][(int)rank * warps + warp];
     if constexpr (SPLIT == 1) {
       if (sub == 0) *mine = total;
       __syncthreads();
@@ -454,9 +460,10 @@ __device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_
       }
       cluster_barrier();
     }
+    // A fixed number of reads: places that no warp writes hold zero.
     total = 0.f;
-#pragma unroll 4
-    for (int w = sub; w < all; w += kLanes) total += slot[idx][w];
+#pragma unroll
+    for (int w = 0; w < Slots<N, SPLIT>::kReads; ++w) total += slot.v[idx][w * kLanes + sub];
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
@@ -490,8 +497,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
   constexpr int W = FP32 ? 2 : 1;              // 16-byte pieces of eight stream values
   constexpr int PIECES = 2 * W + 2;            // h, dh_out, dn, b
   extern __shared__ uint4 shared[];            // [4][T] gate and scale, then [stages][PIECES][T]
-  __shared__ float slots[2][N][kMaxWarps + 32 / N];
-  __shared__ float mean_slots[2][8][kMaxWarps + 4];
+  __shared__ Slots<N, SPLIT> slots[2];
+  __shared__ Slots<8, SPLIT> mean_slots[LAYER ? 2 : 1];
   const int T = (int)blockDim.x, warps = T >> 5, t = (int)threadIdx.x;
   uint32_t rank = 0;
   if constexpr (SPLIT > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -553,7 +560,13 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
     const ulonglong2 y = reinterpret_cast<const ulonglong2*>(shared)[(k + 1) * T + t];
     v[0].v = x.x, v[1].v = x.y, v[2].v = y.x, v[3].v = y.y;
   };
-  if constexpr (SPLIT > 1) cluster_barrier();  // the peers' shared memory is there
+  for (int i = t; i < (int)(sizeof(slots) / 4); i += T) reinterpret_cast<float*>(slots)[i] = 0.f;
+  if constexpr (LAYER) {
+    for (int i = t; i < (int)(sizeof(mean_slots) / 4); i += T) reinterpret_cast<float*>(mean_slots)[i] = 0.f;
+  }
+  // The slots are cleared, the peers' too.
+  if constexpr (SPLIT > 1) cluster_barrier();
+  else __syncthreads();
 
   int buf = 0, stage = 0;
   for (int64_t row = first; row < last; ++row, buf ^= 1) {
@@ -629,8 +642,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
       q[k] = h.x + h.y;
     }
     row_group_sums<N, SPLIT>(q, warps, rank, slots[buf]);
-    const float rx = a.dn ? 1.0f / sqrtf(q[0] * inv_d + a.eps) : 0.f;
-    const float ru = a.post == kNone ? 1.0f : 1.0f / sqrtf(q[1] * inv_d + a.eps);
+    const float rx = a.dn ? rsqrtf(q[0] * inv_d + a.eps) : 0.f;
+    const float ru = a.post == kNone ? 1.0f : rsqrtf(q[1] * inv_d + a.eps);
     const float k = rx * rx * rx * (q[2] * inv_d);
     float mg = 0.f, mw = 0.f, swu = q[3] + rx * q[4] - k * q[5];
     if constexpr (LAYER) {
