@@ -329,7 +329,8 @@ lg_status lg_block_norm_backward(const lg_block_norm_backward_args* a, void* wor
                                       a->dh,     a->db,     a->dgate,  a->dscale, a->dshift,
                                       reinterpret_cast<float*>(workspace),
                                       a->M,      a->segment_tokens,    a->D,      a->stream_type == LG_STREAM_FP32,
-                                      a->post,   a->pre,    a->alpha,  a->eps};
+                                      a->post,   a->pre,    a->alpha,  a->eps,
+                                      g_wait_limit_ns.load(std::memory_order_relaxed)};
   int kernels = 0;
   const cudaError_t e = lg::launch_block_norm_backward(p, &kernels, as_stream(stream));
   return launched(e, (uint64_t)kernels);

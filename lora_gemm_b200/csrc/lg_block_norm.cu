@@ -23,8 +23,11 @@
 // columns, so the column sums dgate, dscale and dshift stay in registers over
 // the CTA's rows; one partial row per CTA goes to the workspace and a second
 // kernel adds the partials of a segment in a fixed order.
+#include <initializer_list>
+
 #include "lg_internal.h"
 #include "lg_mx.cuh"
+#include "lg_pipeline.cuh"
 
 namespace lg {
 
@@ -363,8 +366,20 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
 // Backward.
 // ---------------------------------------------------------------------------
 constexpr int kBackStagesMax = 4;
-constexpr int kBackThreads = 448;              // at most, of eight columns each
-constexpr size_t kBackSmem = 106 * 1024;  // modulation and row stages: two CTAs per SM
+// A backward CTA: at most 448 threads (of eight columns each), two per SM, so 72
+// registers a thread.  FP32 rows hold more of them (spills at 72): where one CTA
+// of up to 256 threads has the row, three per SM, 80 registers (33001 x 1024: 166
+// us against 207); a wider row on more CTAs of that size loses more to their
+// meeting (33001 x 7168 on four: 1423 us against 1050 on two).
+constexpr int kBackThreads = 448;
+constexpr int kBackSmem = 106 * 1024;  // modulation and row stages
+template <bool FP32, int SPLIT>
+struct Back {
+  static constexpr bool kNarrow = FP32 && SPLIT == 1;
+  static constexpr int kThreads = kNarrow ? 256 : kBackThreads;
+  static constexpr int kCtas = kNarrow ? 3 : 2;
+  static constexpr int kSmem = kNarrow ? 70 * 1024 : kBackSmem;
+};
 
 struct BackArgs {
   const void* dn;
@@ -384,6 +399,7 @@ struct BackArgs {
   int64_t chunk_rows;
   int D, post, pre, stages;
   float alpha, eps;
+  unsigned long long wait_limit_ns;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -403,72 +419,89 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Sums of N = 8 or 16 values over all threads of the SPLIT CTAs that share a
-// row, in every thread.  Within a warp each step exchanges half of the values a
-// lane still holds with the lane whose bit differs (9 shuffles for 8 values
-// instead of 40): value i ends in lanes i * 32 / N and up.  Every warp leaves its
-// sums in all SPLIT CTAs' `slot`, at the same place, so that all
-// add them up in the same order; `slot` is not written again before the next
-// but one call.  (Its rows are 32 / N words longer than 64: the lanes'
-// reads then fall into different banks.)
-template <int N, int SPLIT>
+// One 32-bit value into a CTA of the cluster, counted on that CTA's mbarrier: the
+// barrier's completion makes it visible, without a fence that would also wait
+// for this thread's stores to global memory.
+__device__ __forceinline__ void store_async(uint32_t cluster_addr, float v, uint32_t cluster_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
+               "r"(__float_as_uint(v)), "r"(cluster_bar)
+               : "memory");
+}
+
+// What the warps of a row's CTAs need to meet: the places of their sums, and the
+// mbarrier that counts their arrival (SPLIT > 1).  A pair of these alternates
+// from row to row: a CTA writes a peer's slot for the next row but one only
+// after that peer's warps have all sent the row between, having read this one.
+// Sums of N <= 8 values over all threads of the SPLIT CTAs that share a row, in
+// every thread.  Within a warp each step exchanges half of the eight values a
+// lane still holds with the lane whose bit differs (9 shuffles instead of 40):
+// value i ends in lanes 4 i .. 4 i + 3.  Every warp leaves its sums in all
+// SPLIT CTAs' slot, at the same place, so that all add them up in the same order.
+template <int SPLIT>
 struct Slots {
-  static constexpr int kWarps = SPLIT * (SPLIT == 8 ? 8 : kBackThreads / 32);  // at most, of a row
-  static constexpr int kLanes = 32 / N;                                        // lanes that share a value
-  static constexpr int kReads = (kWarps + kLanes - 1) / kLanes;
-  static constexpr int kStride = 64 + kLanes;
-  float v[N][kStride];
+  static constexpr int kWarps = SPLIT * (SPLIT == 8 ? 8 : 14);  // at most, of a row
+  static constexpr int kReads = (kWarps + 3) / 4;
+  float v[8][68];  // 64 warps and four more: eight rows of four reads fall into 32 banks
+  uint64_t bar;
 };
-template <int N, int SPLIT>
-__device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_t rank, Slots<N, SPLIT>& slot) {
+// False when the wait for the peers ran out.
+template <int SPLIT, int N>
+__device__ __forceinline__ bool row_group_sums(float (&sum)[N], int warps, uint32_t rank, Slots<SPLIT>& slot,
+                                               uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  bool ok = true;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int half = N / 2;
+  float v[8];
 #pragma unroll
-  for (int bit = 16; bit > 0; bit >>= 1) {
-    if (half >= 1) {
-      const bool up = lane & bit;
+  for (int i = 0; i < 8; ++i) v[i] = i < N ? sum[i] : 0.f;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if (i < half) {
-          const float give = up ? v[i] : v[i + half];
-          const float keep = up ? v[i + half] : v[i];
-          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
-        }
-      }
-      half >>= 1;
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  for (int half = 4; half >= 1; half >>= 1) {
+    const bool up = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[i + half];
+      const float keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
     }
   }
-  constexpr int kLanes = Slots<N, SPLIT>::kLanes;
   float total = v[0];
+  total += __shfl_xor_sync(0xffffffffu, total, 2);
+  total += __shfl_xor_sync(0xffffffffu, total, 1);
   if (SPLIT > 1 || warps > 1) {
-    const int idx = lane / kLanes, sub = lane % kLanes;
+    const int idx = lane >> 2, sub = lane & 3;
     float* mine = &slot.v[idx][(int)rank * warps + warp];
     if constexpr (SPLIT == 1) {
       if (sub == 0) *mine = total;
       __syncthreads();
     } else {
+      const uint32_t bar = smem_u32(&slot.bar);
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(SPLIT * warps * 8 * 4));
       if (sub == 0) {
-        const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine);
+        const uint32_t at = smem_u32(mine);
 #pragma unroll
-        for (uint32_t c = 0; c < SPLIT; ++c) {
-          uint32_t peer;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(c));
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer), "f"(total) : "memory");
-        }
+        for (uint32_t c = 0; c < SPLIT; ++c) store_async(mapa_shared(at, c), total, mapa_shared(bar, c));
       }
-      cluster_barrier();
+      ok = wait_bounded(bar, parity, limit_ns, abort_flag, true);
+      __syncwarp();
     }
     // A fixed number of reads: places that no warp writes hold zero.
     total = 0.f;
 #pragma unroll
-    for (int w = 0; w < Slots<N, SPLIT>::kReads; ++w) total += slot.v[idx][w * kLanes + sub];
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int w = 0; w < Slots<SPLIT>::kReads; ++w) total += slot.v[idx][4 * w + sub];
+    total += __shfl_xor_sync(0xffffffffu, total, 2);
+    total += __shfl_xor_sync(0xffffffffu, total, 1);
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, total, i * kLanes);
+  for (int i = 0; i < N; ++i) sum[i] = __shfl_sync(0xffffffffu, total, 4 * i);
+  return ok;
+}
+// The two halves of N pairs added up.
+template <int N>
+__device__ __forceinline__ void fold(const F2 (&p)[N], float (&q)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 h = split(p[i]);
+    q[i] = h.x + h.y;
+  }
 }
 
 // A cluster of SPLIT CTAs: consecutive rows of one segment; every thread always
@@ -482,23 +515,25 @@ __device__ __forceinline__ void row_group_sums(float (&v)[N], int warps, uint32_
 // are laid out in shared memory by thread (read in place, a thread's eight FP32
 // values are 32 bytes from its neighbour's and every load takes twice the passes).
 //
-// All row sums come from one pass (two with a layer norm, whose means are
-// taken first so that the squares are those of centred values).  With x, b the
-// centred rows (RMS: the rows), g = dn (1 + scale), t = gate:
+// Without a layer norm all row sums come from one pass.  With x, b the rows, g =
+// dn (1 + scale), t = gate:
 //   rx^2 = D / sum x^2, ru^2 = D / sum b^2 (+ eps),   k = rx^3 mean(g x)
 //   dh' = dh_out + rx (g - mean g) - k x,   w = t dh',  u = ru b
 //   sum w u = ru (sum t b dh_out + rx (sum t b g - mean g sum t b) - k sum t b x)
-//   sum w   =     sum t dh_out   + rx (sum t g   - mean g sum t)   - k sum t x
 //   db = ru (w - mean w - u mean(w u))
-// so the second norm's sums need no second pass over the first one's result.
-template <bool FP32, int SPLIT, bool LAYER>
-__global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const BackArgs a) {
-  constexpr int N = LAYER ? 16 : 8;
+// so the second norm's sums need no second pass over the first one's result
+// (mean g and mean w belong to layer norms).  A layer norm's row is centred
+// first, so that its squares are those of centred values (a mean far above the
+// deviation would cancel in FP32): its mean takes a pass.  After a layer norm on
+// the block's output the second norm's sums are taken from dh' itself, in a pass
+// of their own: that is eight sums less to hold than the closed form.
+template <bool FP32, int SPLIT, bool PRE_L, bool POST_L>
+__global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>::kCtas) k_block_norm_backward(const BackArgs a) {
   constexpr int W = FP32 ? 2 : 1;              // 16-byte pieces of eight stream values
   constexpr int PIECES = 2 * W + 2;            // h, dh_out, dn, b
-  extern __shared__ uint4 shared[];            // [4][T] gate and scale, then [stages][PIECES][T]
-  __shared__ Slots<N, SPLIT> slots[2];
-  __shared__ Slots<8, SPLIT> mean_slots[LAYER ? 2 : 1];
+  extern __shared__ uint4 shared[];            // [4][T] scale and gate, then [stages][PIECES][T]
+  constexpr int PASSES = 1 + (PRE_L ? 1 : 0) + (POST_L ? 1 : 0);
+  __shared__ Slots<SPLIT> slots[2][PASSES];
   const int T = (int)blockDim.x, warps = T >> 5, t = (int)threadIdx.x;
   uint32_t rank = 0;
   if constexpr (SPLIT > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -515,21 +550,33 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
 
   uint4* ring = shared + 4 * T;
   auto piece = [&](int stage, int k) { return &ring[(stage * PIECES + k) * T + t]; };
+  // The stream's pieces: bf16, each thread its own 16 bytes.  FP32, a warp's 1024
+  // bytes in two runs of 512: lane l copies pieces (l mod 2) of the threads l / 2
+  // and 16 + l / 2 of its warp, and the warp meets before and after reading.
+  auto fetch_stream = [&](const void* base, int64_t at, int stage, int k) {
+    if constexpr (FP32) {
+      const int lane = t & 31;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int to = (t & ~31) + 16 * w + (lane >> 1);  // thread
+        const int c = ((int)rank * T + to) * 8 + 4 * (lane & 1);
+        if (c < a.D)
+          cp_async16(smem_addr(&ring[(stage * PIECES + k + (lane & 1)) * T + to]),
+                     reinterpret_cast<const float*>(base) + (at - col) + c);
+      }
+    } else {
+      if (live) cp_async16(smem_addr(piece(stage, k)), reinterpret_cast<const uint16_t*>(base) + at);
+    }
+  };
   auto fetch = [&](int64_t row, int stage) {
-    if (row < last && live) {
+    if (row < last) {
       const int64_t at = row * a.D + col;
       if (a.dn) {
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-          cp_async16(smem_addr(piece(stage, w)), reinterpret_cast<const uint8_t*>(a.h) + at * (2 * W) + 16 * w);
-        cp_async16(smem_addr(piece(stage, 2 * W)), reinterpret_cast<const uint8_t*>(a.dn) + at * 2);
+        fetch_stream(a.h, at, stage, 0);
+        if (live) cp_async16(smem_addr(piece(stage, 2 * W)), reinterpret_cast<const uint16_t*>(a.dn) + at);
       }
-      if (a.dh_out) {
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-          cp_async16(smem_addr(piece(stage, W + w)), reinterpret_cast<const uint8_t*>(a.dh_out) + at * (2 * W) + 16 * w);
-      }
-      if (a.b) cp_async16(smem_addr(piece(stage, 2 * W + 1)), reinterpret_cast<const uint8_t*>(a.b) + at * 2);
+      if (a.dh_out) fetch_stream(a.dh_out, at, stage, W);
+      if (a.b && live) cp_async16(smem_addr(piece(stage, 2 * W + 1)), reinterpret_cast<const uint16_t*>(a.b) + at);
     }
     cp_async_commit();  // a group per row, empty past the last one
   };
@@ -545,32 +592,43 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) *piece(st, k) = make_uint4(0, 0, 0, 0);
   }
+  __syncwarp();
   for (int st = 0; st < a.stages; ++st) fetch(first + st, st);
-  // Gate in pieces 0 and 1 of this thread, scale in 2 and 3.
+  // Scale in pieces 0 and 1 of this thread, gate in 2 and 3.
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float* m = k < 2 ? a.gate : a.scale;
-    float4 v = k < 2 ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* m = k < 2 ? a.scale : a.gate;
+    float4 v = k < 2 ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(1.f, 1.f, 1.f, 1.f);
     if (m && live) v = __ldg(reinterpret_cast<const float4*>(m + s * a.D + col + 4 * (k & 1)));
-    if (!live) v = make_float4(0.f, 0.f, 0.f, 0.f);
     reinterpret_cast<float4*>(shared)[k * T + t] = v;
   }
-  auto mod = [&](int k, F2 (&v)[4]) {
-    const ulonglong2 x = reinterpret_cast<const ulonglong2*>(shared)[k * T + t];
-    const ulonglong2 y = reinterpret_cast<const ulonglong2*>(shared)[(k + 1) * T + t];
+  auto scale_at = [&](F2 (&v)[4]) {
+    const ulonglong2 x = reinterpret_cast<const ulonglong2*>(shared)[t];
+    const ulonglong2 y = reinterpret_cast<const ulonglong2*>(shared)[T + t];
+    v[0].v = x.x, v[1].v = x.y, v[2].v = y.x, v[3].v = y.y;
+  };
+  auto gate_at = [&](F2 (&v)[4]) {
+    const ulonglong2 x = reinterpret_cast<const ulonglong2*>(shared)[2 * T + t];
+    const ulonglong2 y = reinterpret_cast<const ulonglong2*>(shared)[3 * T + t];
     v[0].v = x.x, v[1].v = x.y, v[2].v = y.x, v[3].v = y.y;
   };
   for (int i = t; i < (int)(sizeof(slots) / 4); i += T) reinterpret_cast<float*>(slots)[i] = 0.f;
-  if constexpr (LAYER) {
-    for (int i = t; i < (int)(sizeof(mean_slots) / 4); i += T) reinterpret_cast<float*>(mean_slots)[i] = 0.f;
+  __shared__ int abort_word;
+  if (t == 0) abort_word = 0;
+  volatile int* abort_flag = &abort_word;
+  __syncthreads();
+  if constexpr (SPLIT > 1) {
+    if (t == 0) {
+      for (int k = 0; k < 2 * PASSES; ++k) mbar_init(smem_u32(&slots[0][0].bar) + k * (uint32_t)sizeof(Slots<SPLIT>), 1);
+      fence_mbarrier_init();
+    }
+    cluster_barrier();  // every CTA's slots and barriers are ready
   }
-  // The slots are cleared, the peers' too.
-  if constexpr (SPLIT > 1) cluster_barrier();
-  else __syncthreads();
 
   int buf = 0, stage = 0;
   for (int64_t row = first; row < last; ++row, buf ^= 1) {
     cp_async_wait(a.stages - 1);
+    if constexpr (FP32) __syncwarp();
     Raw8<FP32> rx8, rd8;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -578,106 +636,190 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
       rd8.q[w] = *piece(stage, W + w);
     }
     const uint4 rn8 = *piece(stage, 2 * W), rb8 = *piece(stage, 2 * W + 1);
+    if constexpr (FP32) __syncwarp();
     fetch(row + a.stages, stage);
     if (++stage == a.stages) stage = 0;
 
-    float mx = 0.f, mu = 0.f;
-    if constexpr (LAYER) {
-      F2 sx = f2(0.f, 0.f), su = sx, x[4], u[4];
-      rx8.get(x);
-      unpack8(rb8, u);
+    Slots<SPLIT>* slot = slots[buf];
+    const uint32_t parity = (uint32_t)((row - first) >> 1) & 1u;
+    bool ok = true;
+    const F2 zero = f2(0.f, 0.f);
+    float mx = 0.f, mu = 0.f, rx = 0.f, ru = 1.f, k = 0.f, mg = 0.f, mw = 0.f, mwu = 0.f;
+
+    if constexpr (POST_L) {
+      // The mean of b with, layer pre-norm: the means of x and g; else the sums of x.
+      F2 p[3] = {zero, zero, zero};
+      if (live) {
+        F2 x[4], g[4], u[4], sc[4];
+        rx8.get(x);
+        unpack8(rn8, g);
+        unpack8(rb8, u);
+        scale_at(sc);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sx = sx + x[i];
-        su = su + u[i];
-      }
-      float m[8] = {};
-      m[0] = split(sx).x + split(sx).y;
-      m[1] = split(su).x + split(su).y;
-      row_group_sums<8, SPLIT>(m, warps, rank, mean_slots[buf]);
-      if (a.pre == kLayer) mx = m[0] * inv_d;
-      if (a.post == kLayer) mu = m[1] * inv_d;
-    }
-    const F2 nmx = f2(-mx, -mx), nmu = f2(-mu, -mu);
-    F2 p[LAYER ? 12 : 6];
-#pragma unroll
-    for (int k = 0; k < (LAYER ? 12 : 6); ++k) p[k] = f2(0.f, 0.f);
-    if (live) {
-      F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
-      rx8.get(x);
-      rd8.get(d);
-      unpack8(rn8, g);
-      unpack8(rb8, u);
-      mod(2, sc);
-      mod(0, gt);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2][i] = acc[2][i] + g[i];
-        const F2 w = fma(g[i], sc[i], g[i]);
-        if constexpr (LAYER) {
-          x[i] = x[i] + nmx;
-          u[i] = u[i] + nmu;
-        }
-        const F2 tb = gt[i] * u[i];
-        p[0] = fma(x[i], x[i], p[0]);
-        p[1] = fma(u[i], u[i], p[1]);
-        p[2] = fma(w, x[i], p[2]);
-        p[3] = fma(tb, d[i], p[3]);
-        p[4] = fma(tb, w, p[4]);
-        p[5] = fma(tb, x[i], p[5]);
-        if constexpr (LAYER) {
-          p[6] = p[6] + w;
-          p[7] = p[7] + tb;
-          p[8] = fma(gt[i], d[i], p[8]);
-          p[9] = fma(gt[i], w, p[9]);
-          p[10] = p[10] + gt[i];
-          p[11] = fma(gt[i], x[i], p[11]);
+        for (int i = 0; i < 4; ++i) {
+          const F2 w = fma(g[i], sc[i], g[i]);
+          p[0] = p[0] + u[i];
+          p[1] = PRE_L ? p[1] + x[i] : fma(x[i], x[i], p[1]);
+          p[2] = PRE_L ? p[2] + w : fma(w, x[i], p[2]);
         }
       }
-    }
-    float q[N] = {};
+      float q[3];
+      fold(p, q);
+      ok = row_group_sums<SPLIT>(q, warps, rank, slot[0], parity, a.wait_limit_ns, abort_flag) && ok;
+      mu = q[0] * inv_d;
+      if constexpr (PRE_L) {
+        mx = q[1] * inv_d;
+        mg = q[2] * inv_d;
+        const F2 nmx = f2(-mx, -mx);
+        F2 s[2] = {zero, zero};
+        if (live) {
+          F2 x[4], g[4], sc[4];
+          rx8.get(x);
+          unpack8(rn8, g);
+          scale_at(sc);
 #pragma unroll
-    for (int k = 0; k < (LAYER ? 12 : 6); ++k) {
-      const float2 h = split(p[k]);
-      q[k] = h.x + h.y;
+          for (int i = 0; i < 4; ++i) {
+            x[i] = x[i] + nmx;
+            s[0] = fma(x[i], x[i], s[0]);
+            s[1] = fma(fma(g[i], sc[i], g[i]), x[i], s[1]);
+          }
+        }
+        float r[2];
+        fold(s, r);
+        ok = row_group_sums<SPLIT>(r, warps, rank, slot[PASSES - 1], parity, a.wait_limit_ns, abort_flag) && ok;
+        q[1] = r[0];
+        q[2] = r[1];
+      }
+      if (a.dn) {
+        rx = rsqrtf(q[1] * inv_d + a.eps);
+        k = rx * rx * rx * (q[2] * inv_d);
+      }
+    } else {
+      if constexpr (PRE_L) {
+        F2 p[2] = {zero, zero};
+        if (live) {
+          F2 x[4], g[4], sc[4];
+          rx8.get(x);
+          unpack8(rn8, g);
+          scale_at(sc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[0] = p[0] + x[i];
+            p[1] = p[1] + fma(g[i], sc[i], g[i]);
+          }
+        }
+        float q[2];
+        fold(p, q);
+        ok = row_group_sums<SPLIT>(q, warps, rank, slot[0], parity, a.wait_limit_ns, abort_flag) && ok;
+        mx = q[0] * inv_d;
+        mg = q[1] * inv_d;
+      }
+      const F2 nmx = f2(-mx, -mx);
+      F2 p[PRE_L ? 7 : 6];
+#pragma unroll
+      for (int i = 0; i < (PRE_L ? 7 : 6); ++i) p[i] = zero;
+      if (live) {
+        F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
+        rx8.get(x);
+        rd8.get(d);
+        unpack8(rn8, g);
+        unpack8(rb8, u);
+        scale_at(sc);
+        gate_at(gt);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (PRE_L) x[i] = x[i] + nmx;
+          acc[2][i] = acc[2][i] + g[i];
+          const F2 w = fma(g[i], sc[i], g[i]);
+          const F2 tb = gt[i] * u[i];
+          p[0] = fma(x[i], x[i], p[0]);
+          p[1] = fma(u[i], u[i], p[1]);
+          p[2] = fma(w, x[i], p[2]);
+          p[3] = fma(tb, d[i], p[3]);
+          p[4] = fma(tb, w, p[4]);
+          p[5] = fma(tb, x[i], p[5]);
+          if constexpr (PRE_L) p[6] = p[6] + tb;
+        }
+      }
+      float q[PRE_L ? 7 : 6];
+      fold(p, q);
+      ok = row_group_sums<SPLIT>(q, warps, rank, slot[PASSES - 1], parity, a.wait_limit_ns, abort_flag) && ok;
+      if (a.dn) {
+        rx = rsqrtf(q[0] * inv_d + a.eps);
+        k = rx * rx * rx * (q[2] * inv_d);
+      }
+      if (a.post != kNone) {
+        ru = rsqrtf(q[1] * inv_d + a.eps);
+        float swu = q[3] + rx * q[4] - k * q[5];
+        if constexpr (PRE_L) swu -= rx * mg * q[6];
+        mwu = ru * swu * inv_d;
+      }
     }
-    row_group_sums<N, SPLIT>(q, warps, rank, slots[buf]);
-    const float rx = a.dn ? rsqrtf(q[0] * inv_d + a.eps) : 0.f;
-    const float ru = a.post == kNone ? 1.0f : rsqrtf(q[1] * inv_d + a.eps);
-    const float k = rx * rx * rx * (q[2] * inv_d);
-    float mg = 0.f, mw = 0.f, swu = q[3] + rx * q[4] - k * q[5];
-    if constexpr (LAYER) {
-      if (a.pre == kLayer) mg = q[6] * inv_d;
-      swu -= rx * mg * q[7];
-      if (a.post == kLayer) mw = inv_d * (q[8] + rx * (q[9] - mg * q[10]) - k * q[11]);
-    }
-    const float mwu = a.post == kNone ? 0.f : ru * swu * inv_d;  // mean of w u
-    const F2 rx2 = f2(rx, rx), nk2 = f2(-k, -k), ru2 = f2(ru, ru), nmg2 = f2(-rx * mg, -rx * mg);
-    const F2 alpha2 = f2(a.alpha, a.alpha), nmw2 = f2(-ru * mw, -ru * mw), nmwu2 = f2(-ru * mwu, -ru * mwu);
-    if (live) {
-      F2 x[4], d[4], g[4], u[4], sc[4], gt[4];
-      rx8.get(x);
+
+    const F2 rx2 = f2(rx, rx), nk2 = f2(-k, -k), nmx2 = f2(-mx, -mx), nmg2 = f2(-rx * mg, -rx * mg);
+    const F2 alpha2 = f2(a.alpha, a.alpha), nmu2 = f2(-mu, -mu);
+    F2 d[4];
+    // dh', from the row's data and statistics.
+    auto stream_gradient = [&](F2 (&x)[4], F2 (&g)[4], const F2 (&sc)[4]) {
       rd8.get(d);
-      unpack8(rn8, g);
-      unpack8(rb8, u);
-      mod(2, sc);
-      mod(0, gt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (LAYER) {
-          x[i] = x[i] + nmx;
-          u[i] = u[i] + nmu;
-        }
-        u[i] = u[i] * ru2;
+        if constexpr (PRE_L) x[i] = x[i] + nmx2;
         const F2 rg = rx2 * g[i];
         acc[1][i] = fma(rg, x[i], acc[1][i]);
         d[i] = fma(rg, sc[i], rg + d[i]);
-        if constexpr (LAYER) d[i] = d[i] + nmg2;
+        if constexpr (PRE_L) d[i] = d[i] + nmg2;
         d[i] = fma(nk2, x[i], d[i]);
+      }
+    };
+    if constexpr (POST_L) {
+      F2 p[3] = {zero, zero, zero};
+      if (live) {
+        F2 x[4], g[4], u[4], sc[4], gt[4];
+        rx8.get(x);
+        unpack8(rn8, g);
+        scale_at(sc);
+        stream_gradient(x, g, sc);
+        unpack8(rb8, u);
+        gate_at(gt);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[2][i] = acc[2][i] + g[i];
+          u[i] = u[i] + nmu2;
+          const F2 w = gt[i] * d[i];
+          p[0] = fma(u[i], u[i], p[0]);
+          p[1] = fma(w, u[i], p[1]);
+          p[2] = p[2] + w;
+        }
+      }
+      float q[3];
+      fold(p, q);
+      ok = row_group_sums<SPLIT>(q, warps, rank, slot[1], parity, a.wait_limit_ns, abort_flag) && ok;
+      ru = rsqrtf(q[0] * inv_d + a.eps);
+      mwu = ru * q[1] * inv_d;
+      mw = q[2] * inv_d;
+    }
+    // A wait that ran out is recorded; every CTA of the cluster ends the same way.
+    if (SPLIT > 1 && !__all_sync(0xffffffffu, ok)) break;
+    const F2 ru2 = f2(ru, ru), nmw2 = f2(-ru * mw, -ru * mw), nmwu2 = f2(-ru * mwu, -ru * mwu);
+    if (live) {
+      F2 x[4], g[4], u[4], sc[4], gt[4];
+      if constexpr (!POST_L) {
+        rx8.get(x);
+        unpack8(rn8, g);
+        scale_at(sc);
+        stream_gradient(x, g, sc);
+      }
+      unpack8(rb8, u);
+      gate_at(gt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (POST_L) u[i] = u[i] + nmu2;
+        u[i] = u[i] * ru2;
         acc[0][i] = fma(d[i], u[i], acc[0][i]);
         const F2 w = (ru2 * gt[i]) * d[i];
         u[i] = fma(nmwu2, u[i], w);
-        if constexpr (LAYER) u[i] = u[i] + nmw2;
+        if constexpr (POST_L) u[i] = u[i] + nmw2;
         d[i] = d[i] * alpha2;
       }
       const int64_t at = row * a.D + col;
@@ -686,6 +828,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) k_block_norm_backward(const B
     }
   }
   cp_async_wait(0);
+  // No CTA leaves while a peer may still send it sums.
+  if constexpr (SPLIT > 1) cluster_barrier();
   if (!live) return;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -765,13 +909,16 @@ cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
 }
 
 // CTAs that share a row in the backward pass, and their threads.
+template <bool FP32>
 int back_split(int D) {
-  int split = 1;
+  if (D / 8 <= Back<FP32, 1>::kThreads) return 1;
+  int split = 2;
   while ((D / 8 + split - 1) / split > kBackThreads) split *= 2;
   return split;
 }
+template <bool FP32>
 int back_threads(int D) {
-  const int split = back_split(D);
+  const int split = back_split<FP32>(D);
   return 32 * ((D / 8 + 32 * split - 1) / (32 * split));
 }
 
@@ -780,16 +927,18 @@ int back_threads(int D) {
 struct Chunks {
   int64_t segments, rows, per, total;
 };
+template <bool FP32>
 Chunks back_chunks(int64_t M, int D, int64_t seg) {
   if (seg > M) seg = M;
   Chunks c;
   c.segments = (M + seg - 1) / seg;
   const int64_t rest = M - (c.segments - 1) * seg;
-  // One wave: the clusters that 148 SMs hold at 72 registers a thread.  A
+  // One wave: the clusters that 148 SMs hold (at most eight CTAs each).  A
   // chunk's partial sums cost as much traffic as about one of its rows, and its
   // rows follow one another: not less than four of them.
-  const int64_t resident = 2 * kBackThreads / back_threads(D);
-  const int64_t target = 148 * (resident > 8 ? 8 : resident) / back_split(D);
+  const int split = back_split<FP32>(D), threads = back_threads<FP32>(D);
+  const int64_t resident = (split == 1 ? Back<FP32, 1>::kCtas * Back<FP32, 1>::kThreads : 2 * kBackThreads) / threads;
+  const int64_t target = 148 * (resident > 8 ? 8 : resident) / split;
   c.rows = (M + target - 1) / target;
   if (c.rows < 4) c.rows = 4;
   if (c.rows > seg) c.rows = seg;
@@ -830,20 +979,25 @@ cudaError_t launch_block_norm(const BlockNormLaunch& p, cudaStream_t s) {
 }
 
 size_t block_norm_backward_workspace(int64_t M, int D, int64_t segment_tokens) {
-  const Chunks c = back_chunks(M, D, segment_tokens);
-  return c.per == 1 ? 0 : (size_t)c.total * 3 * D * sizeof(float);  // one chunk per segment: nothing to add up
+  // The larger of the two stream types'.  One chunk per segment: nothing to add up.
+  size_t most = 0;
+  for (const Chunks& c : {back_chunks<false>(M, D, segment_tokens), back_chunks<true>(M, D, segment_tokens)}) {
+    const size_t bytes = c.per == 1 ? 0 : (size_t)c.total * 3 * D * sizeof(float);
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 namespace {
 
-template <bool FP32, int SPLIT, bool LAYER>
+template <bool FP32, int SPLIT, bool PRE_L, bool POST_L>
 cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
   const size_t mods = (size_t)64 * T, stage = (size_t)(FP32 ? 6 : 4) * 16 * T;
-  int stages = (int)((kBackSmem - mods) / stage);
+  int stages = (int)((Back<FP32, SPLIT>::kSmem - mods) / stage);
   if (stages > kBackStagesMax) stages = kBackStagesMax;
   if (stages > a.chunk_rows) stages = (int)a.chunk_rows;
   a.stages = stages;
-  const cudaError_t e = allow_shared_memory((const void*)k_block_norm_backward<FP32, SPLIT, LAYER>, (int)kBackSmem);
+  const cudaError_t e = allow_shared_memory((const void*)k_block_norm_backward<FP32, SPLIT, PRE_L, POST_L>, Back<FP32, SPLIT>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(chunks * SPLIT), 1, 1);
@@ -857,19 +1011,22 @@ cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_block_norm_backward<FP32, SPLIT, LAYER>, (const BackArgs)a);
+  return cudaLaunchKernelEx(&cfg, k_block_norm_backward<FP32, SPLIT, PRE_L, POST_L>, (const BackArgs)a);
 }
 
 template <bool FP32, int SPLIT>
 cudaError_t back_kind(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
-  const bool layer = a.pre == kLayer || a.post == kLayer;
-  return layer ? back_launch<FP32, SPLIT, true>(a, chunks, T, s) : back_launch<FP32, SPLIT, false>(a, chunks, T, s);
+  const bool pre = a.pre == kLayer, post = a.post == kLayer;
+  if (post) {
+    return pre ? back_launch<FP32, SPLIT, true, true>(a, chunks, T, s) : back_launch<FP32, SPLIT, false, true>(a, chunks, T, s);
+  }
+  return pre ? back_launch<FP32, SPLIT, true, false>(a, chunks, T, s) : back_launch<FP32, SPLIT, false, false>(a, chunks, T, s);
 }
 
 template <bool FP32>
 cudaError_t back_dispatch(BackArgs& a, int64_t chunks, cudaStream_t s) {
-  const int T = back_threads(a.D);
-  switch (back_split(a.D)) {
+  const int T = back_threads<FP32>(a.D);
+  switch (back_split<FP32>(a.D)) {
     case 1: return back_kind<FP32, 1>(a, chunks, T, s);
     case 2: return back_kind<FP32, 2>(a, chunks, T, s);
     case 4: return back_kind<FP32, 4>(a, chunks, T, s);
@@ -880,7 +1037,7 @@ cudaError_t back_dispatch(BackArgs& a, int64_t chunks, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* kernels, cudaStream_t s) {
-  const Chunks c = back_chunks(p.M, p.D, p.segment_tokens);
+  const Chunks c = p.fp32 ? back_chunks<true>(p.M, p.D, p.segment_tokens) : back_chunks<false>(p.M, p.D, p.segment_tokens);
   BackArgs a;
   a.dn = p.dn;
   a.dh_out = p.dh_out;
@@ -900,6 +1057,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* ke
   a.pre = p.pre;
   a.alpha = p.alpha;
   a.eps = p.eps;
+  a.wait_limit_ns = p.wait_limit_ns;
   float* const out[3] = {p.dgate, p.dscale, p.dshift};
   const bool direct = c.per == 1;
   for (int k = 0; k < 3; ++k) a.sums[k] = !out[k] ? nullptr : (direct ? out[k] : p.workspace + (int64_t)k * p.D);
@@ -919,5 +1077,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* ke
   *kernels = 2;
   return cudaGetLastError();
 }
+
+cudaError_t take_norm_error(int* value) { return take_device_error(value); }
 
 }  // namespace lg

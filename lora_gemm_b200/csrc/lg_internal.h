@@ -90,6 +90,7 @@ struct BlockNormBackwardLaunch {
   bool fp32;
   int post, pre;
   float alpha, eps;
+  uint64_t wait_limit_ns;
 };
 // Bytes of partial column sums (0: none are needed); M >= 1.
 size_t block_norm_backward_workspace(int64_t M, int D, int64_t segment_tokens);
@@ -146,9 +147,10 @@ void set_variant_override(int v);
 // Device error word of the current device: read and clear (synchronous on s).
 cudaError_t read_and_clear_device_error(cudaStream_t s, int* value);
 
-// The same for the error words of the MXFP4 kernels (no synchronization before).
+// The same for the error words of the MXFP4 and norm kernels (no synchronization before).
 cudaError_t take_tile_error(int* value);
 cudaError_t take_few_error(int* value);
+cudaError_t take_norm_error(int* value);
 
 // lg_lora_linear_mxfp4 on output tiles: h = x A^T into `h` (workspace, M * R
 // bf16) and y = deq(x) deq(W)^T + h B^T, the factors in bf16.  *kernels:

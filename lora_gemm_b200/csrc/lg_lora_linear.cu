@@ -1421,7 +1421,7 @@ cudaError_t read_and_clear_device_error(cudaStream_t s, int* value) {
   *value = 0;
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;
-  for (auto take : {take_device_error, take_tile_error, take_few_error}) {
+  for (auto take : {take_device_error, take_tile_error, take_few_error, take_norm_error}) {
     int v = 0;
     e = take(&v);
     if (e != cudaSuccess) return e;
