@@ -8,10 +8,12 @@
 // HBM; the statistics are FP32 sums over the row held in registers.
 //
 // Forward: one row per group of warps, each thread holding CH chunks of eight
-// consecutive values.  The row's data are read and written past L1, which is
-// left to the modulation vectors: 3 x 4 D bytes that every row of a segment
-// reads again (more than the row itself), and that the rows resident on an SM
-// share there.
+// consecutive values, 64 registers so that four CTAs of a 7168-wide row share an
+// SM.  The row's data are read and written past L1, which is left to the
+// modulation vectors: 3 x 4 D bytes that every row of a segment reads again (more
+// than the row itself), and that the rows resident on an SM share there, in
+// 256-bit loads.  66601 x 7168 bf16: 619 us without codes (94 % of measured HBM),
+// 790 us with MXFP4 codes (79 %: issue slots 69 % busy, the quantizer's share).
 //
 // Backward: with x^ a normalised row, r its reciprocal deviation and g the
 // gradient there, the input's gradient is
@@ -70,7 +72,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Two FP32 values in a register pair, for the instructions that work on both.
+// Two FP32 values in a register pair, for the instructions that work on both
+// (the backward pass; the forward one, which waits for memory, ran slower so).
 struct F2 {
   uint64_t v;
 };
@@ -116,17 +119,38 @@ __device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight FP32 values of a thread are 32 bytes: one 256-bit access where the
+// pointers allow it (`wide`).  As two of 128 bits, each takes every second half
+// of its warp's sectors, and both take the passes of the whole.
+__device__ __forceinline__ void ld_stream8(const float* p, bool wide, uint4& a, uint4& b) {
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p)
+                 : "memory");
+  } else {
+    a = ld_stream(p);
+    b = ld_stream(p + 4);
+  }
+}
+__device__ __forceinline__ void st_stream8(float* p, bool wide, uint4 a, uint4 b) {
+  if (wide) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    st_stream(p, a);
+    st_stream(p + 4, b);
+  }
+}
+
 // Raw bits of eight stream values: 16 bytes (bf16) or 32 (FP32).
 template <bool FP32>
 struct Raw8 {
   uint4 q[FP32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    if constexpr (FP32) {
-      q[0] = ld_stream(reinterpret_cast<const float*>(base) + at);
-      q[1] = ld_stream(reinterpret_cast<const float*>(base) + at + 4);
-    } else {
-      q[0] = ld_stream(reinterpret_cast<const uint16_t*>(base) + at);
-    }
+  __device__ __forceinline__ void load(const void* base, int64_t at, bool wide) {
+    if constexpr (FP32) ld_stream8(reinterpret_cast<const float*>(base) + at, wide, q[0], q[1]);
+    else q[0] = ld_stream(reinterpret_cast<const uint16_t*>(base) + at);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -154,44 +178,48 @@ struct Raw8 {
     }
   }
 };
+// Stores eight values in the stream's type; the scalar form's v becomes what was
+// stored.
 template <bool FP32>
-__device__ __forceinline__ void store_stream8(void* base, int64_t at, const F2 (&v)[4]) {
+__device__ __forceinline__ void store_stream8(void* base, int64_t at, bool wide, float (&v)[8]) {
   if constexpr (FP32) {
-    float* p = reinterpret_cast<float*>(base) + at;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 a = split(v[2 * i]), b = split(v[2 * i + 1]);
-      st_stream(p + 4 * i, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
-                                      __float_as_uint(b.y)));
-    }
-  } else {
-    st_stream(reinterpret_cast<uint16_t*>(base) + at, pack8(v));
-  }
-}
-// Stores eight values in the stream's type; v becomes what was stored.
-template <bool FP32>
-__device__ __forceinline__ void store_stream8(void* base, int64_t at, float (&v)[8]) {
-  if constexpr (FP32) {
-    float* p = reinterpret_cast<float*>(base) + at;
-    st_stream(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-    st_stream(p + 4,
-              make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+    st_stream8(reinterpret_cast<float*>(base) + at, wide,
+               make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+               make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
   } else {
     const uint4 q = pack8(v);
     st_stream(reinterpret_cast<uint16_t*>(base) + at, q);
     unpack8(q, v);
   }
 }
+template <bool FP32>
+__device__ __forceinline__ void store_stream8(void* base, int64_t at, bool wide, const F2 (&v)[4]) {
+  if constexpr (FP32) {
+    uint4 q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = split(v[2 * i]), b = split(v[2 * i + 1]);
+      q[i] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+    st_stream8(reinterpret_cast<float*>(base) + at, wide, q[0], q[1]);
+  } else {
+    st_stream(reinterpret_cast<uint16_t*>(base) + at, pack8(v));
+  }
+}
 // Eight values of a segment's modulation row (cached), or `other` without one.
-__device__ __forceinline__ void load_mod8(const float* base, int64_t at, float other, float (&v)[8]) {
-  if (base) {
+__device__ __forceinline__ void load_mod8(const float* base, int64_t at, bool wide, float other, float (&v)[8]) {
+  if (!base) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = other;
+  } else if (wide) {
+    asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "l"(base + at));
+  } else {
     const float4 a = __ldg(reinterpret_cast<const float4*>(base + at));
     const float4 b = __ldg(reinterpret_cast<const float4*>(base + at + 4));
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = other;
   }
 }
 
@@ -234,6 +262,7 @@ struct NormArgs {
   int64_t rows;  // M, or with codes M rounded up to 128 (the padding's scale bytes are 0)
   int64_t seg;
   int D, post, pre, format;
+  bool wide_stream, wide_mods;  // 32-byte aligned
   float alpha, eps;
 };
 
@@ -273,7 +302,7 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[
 
 // blockDim.x = 32 * warps for one row, or (ONE) several rows of one warp each.
 template <bool FP32, int CH, bool ONE>
-__global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs a) {
+__global__ void __launch_bounds__(ONE ? 128 : 512, ONE ? 1 : 2) k_block_norm(const NormArgs a) {
   __shared__ float slots[4][kMaxWarps];
   const int warps = ONE ? 1 : (int)blockDim.x >> 5;
   const int t = ONE ? (int)threadIdx.x & 31 : (int)threadIdx.x;
@@ -294,7 +323,7 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
     const int col = (c * T + t) * 8;
     live[c] = col < a.D;
     raw[c].zero();
-    if (live[c]) raw[c].load(a.h, at + col);
+    if (live[c]) raw[c].load(a.h, at + col, a.wide_stream);
   }
   if (a.b) {
 #pragma unroll
@@ -309,11 +338,11 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
       if (!live[c]) continue;
       const int col = (c * T + t) * 8;
       float g[8], h[8];
-      load_mod8(a.gate, mod + col, 1.0f, g);
+      load_mod8(a.gate, mod + col, a.wide_mods, 1.0f, g);
       raw[c].get(h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = fmaf(g[i], v[c][i], a.alpha * h[i]);
-      store_stream8<FP32>(a.h_out, at + col, v[c]);
+      store_stream8<FP32>(a.h_out, at + col, a.wide_stream, v[c]);
     }
   } else {
 #pragma unroll
@@ -327,8 +356,8 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
     uint4 q = make_uint4(0, 0, 0, 0);
     if (live[c]) {
       float s[8], f[8];
-      load_mod8(a.scale, mod + col, 0.0f, s);
-      load_mod8(a.shift, mod + col, 0.0f, f);
+      load_mod8(a.scale, mod + col, a.wide_mods, 0.0f, s);
+      load_mod8(a.shift, mod + col, a.wide_mods, 0.0f, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], 1.0f + s[i], f[i]);
       q = pack8(v[c]);
@@ -352,7 +381,6 @@ __global__ void __launch_bounds__(ONE ? 128 : 1024) k_block_norm(const NormArgs 
         sb = mxfp8_scale_byte(m);
         if (live[c]) *reinterpret_cast<uint2*>(a.codes + at + col) = mxfp8_codes8(w, sb);
       }
-      // The four bytes of a K group from its 16 lanes, one store.
       sb |= __shfl_down_sync(0xffffffffu, sb, 4) << 8;
       sb |= __shfl_down_sync(0xffffffffu, sb, 8) << 16;
       if (live[c] && (t & 15) == 0) {
@@ -398,6 +426,7 @@ struct BackArgs {
   int64_t segments;
   int64_t chunk_rows;
   int D, post, pre, stages;
+  bool wide;  // dh is 32-byte aligned
   float alpha, eps;
   unsigned long long wait_limit_ns;
 };
@@ -823,7 +852,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
         d[i] = d[i] * alpha2;
       }
       const int64_t at = row * a.D + col;
-      if (a.dh) store_stream8<FP32>(a.dh, at, d);
+      if (a.dh) store_stream8<FP32>(a.dh, at, a.wide, d);
       if (a.db) st_stream(reinterpret_cast<uint16_t*>(a.db) + at, pack8(u));
     }
   }
@@ -889,6 +918,8 @@ __global__ void __launch_bounds__(256) k_segment_sums(const SumArgs a) {
     __syncthreads();
   }
 }
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 template <bool FP32, int CH>
 cudaError_t norm_launch(const NormArgs& a, int warps, cudaStream_t s) {
@@ -973,6 +1004,8 @@ cudaError_t launch_block_norm(const BlockNormLaunch& p, cudaStream_t s) {
   a.post = p.post;
   a.pre = p.pre;
   a.format = p.codes_format;
+  a.wide_stream = aligned32(p.h) && aligned32(p.h_out);
+  a.wide_mods = aligned32(p.gate) && aligned32(p.scale) && aligned32(p.shift);
   a.alpha = p.alpha;
   a.eps = p.eps;
   return p.fp32 ? norm_dispatch<true>(a, s) : norm_dispatch<false>(a, s);
@@ -1057,6 +1090,7 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* ke
   a.pre = p.pre;
   a.alpha = p.alpha;
   a.eps = p.eps;
+  a.wide = aligned32(p.dh);
   a.wait_limit_ns = p.wait_limit_ns;
   float* const out[3] = {p.dgate, p.dscale, p.dshift};
   const bool direct = c.per == 1;

@@ -151,6 +151,27 @@ def test_in_place_and_neighbours():
     assert (buf[10:] == 5.0).all() and (nb[10:] == 5.0).all()
 
 
+def _shifted(t, by):
+    """The same values at an address `by` elements past a 512-byte boundary."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+    out = buf[by:].view_as(t)
+    out.copy_(t)
+    return out
+
+
+def test_addresses_aligned_to_16_bytes_only():
+    """FP32 rows and modulations 16 bytes off a 32-byte boundary: same bits as aligned ones."""
+    t = _inputs(12, 520, 2, torch.float32, seed=21)
+    s = {k: _shifted(v, 4 if v.dtype == torch.float32 else 8) for k, v in t.items()}
+    for x, y in zip(lg.block_norm(t["h"], t["b"], t["gate"], t["scale"], t["shift"], segment_tokens=7)[:2],
+                    lg.block_norm(s["h"], s["b"], s["gate"], s["scale"], s["shift"], segment_tokens=7,
+                                  h_out=_shifted(t["h"], 4))[:2]):
+        assert torch.equal(x, y)
+    a = lg.block_norm_backward(t["dn"], t["dh"], t["h"], t["b"], t["gate"], t["scale"], segment_tokens=7)
+    b = lg.block_norm_backward(s["dn"], s["dh"], s["h"], s["b"], s["gate"], s["scale"], segment_tokens=7, dh=s["dh"])
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def _check_backward(t, M, D, seg, post, pre, alpha, eps, has_b=True, dh_out=True):
     a = {k: _np64(v) for k, v in t.items()}
     stream = t["h"].dtype
