@@ -509,7 +509,7 @@ __device__ __forceinline__ bool row_group_sums(float (&sum)[N], int warps, uint3
 #pragma unroll
         for (uint32_t c = 0; c < SPLIT; ++c) store_async(mapa_shared(at, c), total, mapa_shared(bar, c));
       }
-      ok = wait_bounded(bar, parity, limit_ns, abort_flag, true);
+      ok = wait_limited(bar, parity, limit_ns, abort_flag, true);
       __syncwarp();
     }
     // A fixed number of reads: places that no warp writes hold zero.

@@ -66,11 +66,24 @@ __device__ __noinline__ void wait_teardown(uint32_t bar, uint32_t parity, volati
   }
 }
 
-// wait_bounded, also for limits below the time that the hardware may hold a
-// plain try_wait by itself (a wait that short is polled from its start).
+// Polls a phase without being held by the hardware, as a plain try_wait may for
+// microseconds; for limits below that time.  One below the timer's own step gives
+// up at the first look.
+__device__ __noinline__ bool wait_polled(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_test_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (limit_ns < 1000ull || globaltimer_ns() - t0 >= limit_ns) {
+      record_timeout(abort_flag);
+      return false;
+    }
+  }
+}
+// wait_bounded, but exact about short limits.
 __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
                                              bool cluster_scope = false) {
-  if (limit_ns < 20000ull) return wait_slow(bar, parity, limit_ns, abort_flag, cluster_scope);
+  if (limit_ns < 20000ull) return wait_polled(bar, parity, limit_ns, abort_flag);
   return wait_bounded(bar, parity, limit_ns, abort_flag, cluster_scope);
 }
 
