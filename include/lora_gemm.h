@@ -89,7 +89,8 @@ uint64_t lg_launch_count(void);
 lg_status lg_get_last_device_error(void* stream);
 
 /* Upper bound, in nanoseconds, on any single wait inside lg_lora_linear's
- * pipeline (default 4e9).  Process-wide; applies to launches made after the
+ * pipeline, and inside those of lg_lora_linear_mxfp4 and
+ * lg_block_norm_backward (default 4e9).  Process-wide; applies to launches made after the
  * call.  0 restores the default.  Meant for fault-injection tests: a tiny
  * limit makes the waits run out so the timeout path can be exercised. */
 void lg_set_wait_limit_ns(uint64_t limit_ns);
@@ -359,8 +360,11 @@ lg_status lg_mxfp4_dequantize(const void* codes, const void* scales, int64_t row
  *
  *   y[M, N] = deq(x_codes) deq(W_codes)^T + (x A_cat^T) B_cat^T
  *
- * The LoRA term comes from the bf16 x, in bf16 with FP32 accumulation, as in
- * lg_lora_linear_mxfp8 (x may be null when R == 0).
+ * The LoRA term comes from the bf16 x (which may be null when R == 0), with
+ * FP32 accumulation throughout: as in lg_lora_linear_mxfp8 from bf16 roundings
+ * of A_cat, of h = x A_cat^T and of B_cat for M > 128; up to 128 tokens h stays
+ * FP32 and the tensor cores read h and B_cat as TF32 (ten fraction bits), so
+ * the last bits of a token's outputs depend on which side of 128 its batch is.
  *
  *   x_codes [M, K / 2], x_scales   lg_mxfp4_quantize(x) (or the codes that
  *                                  lg_block_norm wrote beside x).

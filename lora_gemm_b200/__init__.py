@@ -10,6 +10,7 @@ when the compiled library is missing (build it with
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -506,12 +507,17 @@ def lora_linear_noalloc(x, W, A_cat, B_cat, y):
     return y
 
 
+# The library's size functions, remembered: each is pure host arithmetic, and a
+# foreign call costs more than a short call's other checks together.
+_scale_bytes = functools.lru_cache(4096)(mx_scale_bytes)
+
+
 def mxfp4_quantize(x, codes=None, scales=None):
     """MXFP4 of bf16 rows x [rows, K] along K: (E2M1 codes uint8 [rows, K / 2],
     two per byte, E8M0 scales uint8 in mx_quantize's blocked layout)."""
     _need(x, torch.bfloat16, "x", 2)
     rows, K = x.shape
-    nscales = mx_scale_bytes(rows, K)
+    nscales = _scale_bytes(rows, K)
     if codes is None:
         codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
     else:
@@ -530,7 +536,7 @@ def mxfp4_dequantize(codes, scales, out=None):
     """The bf16 values [rows, K] that MXFP4 codes [rows, K / 2] and scales stand for (exact)."""
     _need(codes, torch.uint8, "codes", 2)
     rows, K = codes.shape[0], 2 * codes.shape[1]
-    _at_least(scales, mx_scale_bytes(rows, K), "scales")
+    _at_least(scales, _scale_bytes(rows, K), "scales")
     if out is None:
         out = codes.new_empty((rows, K), dtype=torch.bfloat16)
     else:
@@ -546,6 +552,9 @@ def lora_linear_mxfp4_workspace_size(M, K, N, R):
     return int(lib.lg_lora_linear_mxfp4_workspace_size(int(M), int(K), int(N), int(R)))
 
 
+_linear_mxfp4_bytes = functools.lru_cache(4096)(lora_linear_mxfp4_workspace_size)
+
+
 def lora_linear_mxfp4(x, x_mx, W_mx, A_cat, B_cat, y=None, workspace=None):
     """lora_linear with the base term as MXFP4 products: x_mx = mxfp4_quantize(x)
     (or the codes block_norm wrote with it), W_mx = mxfp4_quantize(W) (pairs of
@@ -558,8 +567,8 @@ def lora_linear_mxfp4(x, x_mx, W_mx, A_cat, B_cat, y=None, workspace=None):
     M, K, N = xq.shape[0], 2 * xq.shape[1], wq.shape[0]
     if wq.shape[1] != xq.shape[1]:
         raise ValueError(f"W codes must have shape {(N, K // 2)}, got {tuple(wq.shape)}")
-    _at_least(xsf, mx_scale_bytes(M, K), "x scales")
-    _at_least(wsf, mx_scale_bytes(N, K), "W scales")
+    _at_least(xsf, _scale_bytes(M, K), "x scales")
+    _at_least(wsf, _scale_bytes(N, K), "W scales")
     R = 0
     if A_cat is not None and A_cat.numel() > 0:
         _need(A_cat, torch.float32, "A_cat", 2)
@@ -577,7 +586,7 @@ def lora_linear_mxfp4(x, x_mx, W_mx, A_cat, B_cat, y=None, workspace=None):
     else:
         _need(y, torch.bfloat16, "y", 2)
         _shape(y, (M, N), "y")
-    need = lora_linear_mxfp4_workspace_size(M, K, N, R)
+    need = _linear_mxfp4_bytes(M, K, N, R)
     if workspace is None and need > 0:
         workspace = xq.new_empty(need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -652,7 +661,7 @@ def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6
     codes = scales = None
     if quant is not None:
         width = D if quant == "mxfp8" else D // 2
-        nscales = mx_scale_bytes(M, D)
+        nscales = _scale_bytes(M, D)
         if q is None:
             q = (h.new_empty((M, width), dtype=torch.uint8),
                  h.new_empty(nscales, dtype=torch.uint8))
@@ -673,6 +682,9 @@ def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6
 
 def block_norm_backward_workspace_size(M, D, segment_tokens):
     return int(lib.lg_block_norm_backward_workspace_size(int(M), int(D), int(segment_tokens)))
+
+
+_backward_bytes = functools.lru_cache(4096)(block_norm_backward_workspace_size)
 
 
 def block_norm_backward(dn, dh_out, h_out, b=None, gate=None, scale=None, alpha=1.0, eps=1e-6, post="rms", pre="rms",
@@ -716,7 +728,7 @@ def block_norm_backward(dn, dh_out, h_out, b=None, gate=None, scale=None, alpha=
     if dn is not None:
         dscale = h_out.new_empty((S, D), dtype=torch.float32)
         dshift = h_out.new_empty((S, D), dtype=torch.float32)
-    need = block_norm_backward_workspace_size(M, D, seg)
+    need = _backward_bytes(M, D, seg)
     if workspace is None and need > 0:
         workspace = h_out.new_empty(need, dtype=torch.uint8)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
