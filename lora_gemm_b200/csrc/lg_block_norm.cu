@@ -54,6 +54,12 @@ __device__ __forceinline__ void st_stream(void* p, uint4 v) {
                "r"(v.w)
                : "memory");
 }
+__device__ __forceinline__ void st_stream(void* p, uint32_t v) {
+  asm volatile("st.global.L1::no_allocate.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_stream(void* p, uint2 v) {
+  asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+}
 __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -300,49 +306,49 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[
   }
 }
 
-// blockDim.x = 32 * warps for one row, or (ONE) several rows of one warp each.
+// blockDim.x = 32 * warps for one row, or (ONE) several rows of one warp each.  A
+// warp has CH * 256 consecutive columns, so that a thread's chunks lie 256 columns
+// apart and every array needs one address.
 template <bool FP32, int CH, bool ONE>
-__global__ void __launch_bounds__(ONE ? 128 : 512, ONE ? 1 : 2) k_block_norm(const NormArgs a) {
+__global__ void __launch_bounds__(ONE ? 128 : 512, ONE || FP32 ? 1 : 2) k_block_norm(const NormArgs a) {
   __shared__ float slots[4][kMaxWarps];
   const int warps = ONE ? 1 : (int)blockDim.x >> 5;
   const int t = ONE ? (int)threadIdx.x & 31 : (int)threadIdx.x;
-  const int T = 32 * warps;
   const int64_t row = ONE ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   if (row >= a.rows) return;
   if (row >= a.M) {  // the scale bytes of rows past M
-    for (int kb = t; kb < a.D / 32; kb += T) a.scales[mx_scale_offset(row, kb, a.D / 128)] = 0;
+    for (int kb = t; kb < a.D / 32; kb += 32 * warps) a.scales[mx_scale_offset(row, kb, a.D / 128)] = 0;
     return;
   }
-  const int64_t at = row * a.D;
-  const int64_t mod = row / a.seg * a.D;
+  const int col = (t >> 5) * (CH * 256) + (t & 31) * 8;  // of chunk 0
+  const int64_t at = row * a.D + col;
+  const int64_t mod = row / a.seg * a.D + col;
   bool live[CH];
   Raw8<FP32> raw[CH];
   float v[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int col = (c * T + t) * 8;
-    live[c] = col < a.D;
+    live[c] = col + 256 * c < a.D;
     raw[c].zero();
-    if (live[c]) raw[c].load(a.h, at + col, a.wide_stream);
+    if (live[c]) raw[c].load(a.h, at + 256 * c, a.wide_stream);
   }
   if (a.b) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       uint4 q = make_uint4(0, 0, 0, 0);
-      if (live[c]) q = ld_stream(reinterpret_cast<const uint16_t*>(a.b) + at + (c * T + t) * 8);
+      if (live[c]) q = ld_stream(reinterpret_cast<const uint16_t*>(a.b) + at + 256 * c);
       unpack8(q, v[c]);
     }
     if (a.post != kNone) normalise<CH>(v, live, a.post, a.eps, a.D, warps, slots);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (!live[c]) continue;
-      const int col = (c * T + t) * 8;
       float g[8], h[8];
-      load_mod8(a.gate, mod + col, a.wide_mods, 1.0f, g);
+      load_mod8(a.gate, mod + 256 * c, a.wide_mods, 1.0f, g);
       raw[c].get(h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = fmaf(g[i], v[c][i], a.alpha * h[i]);
-      store_stream8<FP32>(a.h_out, at + col, a.wide_stream, v[c]);
+      store_stream8<FP32>(a.h_out, at + 256 * c, a.wide_stream, v[c]);
     }
   } else {
 #pragma unroll
@@ -350,18 +356,19 @@ __global__ void __launch_bounds__(ONE ? 128 : 512, ONE ? 1 : 2) k_block_norm(con
   }
   if (a.pre == kNone) return;
   normalise<CH>(v, live, a.pre, a.eps, a.D, warps, slots + 2);
+  // Chunk c's K group is 2 c after chunk 0's: 1024 bytes on.
+  uint8_t* sf = a.scales + mx_scale_offset(row, col / 128 * 4, a.D / 128);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int col = (c * T + t) * 8;
     uint4 q = make_uint4(0, 0, 0, 0);
     if (live[c]) {
       float s[8], f[8];
-      load_mod8(a.scale, mod + col, a.wide_mods, 0.0f, s);
-      load_mod8(a.shift, mod + col, a.wide_mods, 0.0f, f);
+      load_mod8(a.scale, mod + 256 * c, a.wide_mods, 0.0f, s);
+      load_mod8(a.shift, mod + 256 * c, a.wide_mods, 0.0f, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], 1.0f + s[i], f[i]);
       q = pack8(v[c]);
-      if (a.n) st_stream(reinterpret_cast<uint16_t*>(a.n) + at + col, q);
+      if (a.n) st_stream(reinterpret_cast<uint16_t*>(a.n) + at + 256 * c, q);
     }
     if (a.format != 0) {
       // D is a multiple of 128 here, so four lanes hold one block, all live or all not.
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(ONE ? 128 : 512, ONE ? 1 : 2) k_block_norm(con
       uint32_t sb;
       if (a.format == kCodesMxfp4) {
         sb = mxfp4_scale_byte(mx_block_max(w));
-        if (live[c]) *reinterpret_cast<uint32_t*>(a.codes + (at + col) / 2) = mxfp4_codes8(w, sb);
+        if (live[c]) st_stream(a.codes + at / 2 + 128 * c, mxfp4_codes8(w, sb));
       } else {
         float m = 0.f;
 #pragma unroll
@@ -379,13 +386,12 @@ __global__ void __launch_bounds__(ONE ? 128 : 512, ONE ? 1 : 2) k_block_norm(con
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         sb = mxfp8_scale_byte(m);
-        if (live[c]) *reinterpret_cast<uint2*>(a.codes + at + col) = mxfp8_codes8(w, sb);
+        if (live[c]) st_stream(a.codes + at + 256 * c, mxfp8_codes8(w, sb));
       }
+      // The four bytes of a K group from its 16 lanes, one store.
       sb |= __shfl_down_sync(0xffffffffu, sb, 4) << 8;
       sb |= __shfl_down_sync(0xffffffffu, sb, 8) << 16;
-      if (live[c] && (t & 15) == 0) {
-        *reinterpret_cast<uint32_t*>(a.scales + mx_scale_offset(row, col / 32, a.D / 128)) = sb;
-      }
+      if (live[c] && (t & 15) == 0) st_stream(sf + 1024 * c, sb);
     }
   }
 }
