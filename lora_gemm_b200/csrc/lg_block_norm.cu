@@ -12,8 +12,8 @@
 // SM.  The row's data are read and written past L1, which is left to the
 // modulation vectors: 3 x 4 D bytes that every row of a segment reads again (more
 // than the row itself), and that the rows resident on an SM share there, in
-// 256-bit loads.  66601 x 7168 bf16: 619 us without codes (94 % of measured HBM),
-// 790 us with MXFP4 codes (79 %: issue slots 69 % busy, the quantizer's share).
+// 256-bit loads.  66601 x 7168 bf16: 627 us without codes (93 % of measured HBM),
+// 732 us with MXFP4 codes (85 %: issue slots, the quantizer's share).
 //
 // Backward: with x^ a normalised row, r its reciprocal deviation and g the
 // gradient there, the input's gradient is
@@ -310,7 +310,7 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[
 // warp has CH * 256 consecutive columns, so that a thread's chunks lie 256 columns
 // apart and every array needs one address.
 template <bool FP32, int CH, bool ONE>
-__global__ void __launch_bounds__(ONE ? 128 : 512, ONE || FP32 ? 1 : 2) k_block_norm(const NormArgs a) {
+__global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP32 || CH < 4 ? 1 : 2) k_block_norm(const NormArgs a) {
   __shared__ float slots[4][kMaxWarps];
   const int warps = ONE ? 1 : (int)blockDim.x >> 5;
   const int t = ONE ? (int)threadIdx.x & 31 : (int)threadIdx.x;
@@ -929,8 +929,8 @@ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) ==
 
 template <bool FP32, int CH>
 cudaError_t norm_launch(const NormArgs& a, int warps, cudaStream_t s) {
-  if (warps == 1) {
-    k_block_norm<FP32, CH, true><<<(unsigned)((a.rows + 3) / 4), 128, 0, s>>>(a);
+  if (CH < 4 && warps == 1) {
+    k_block_norm<FP32, CH < 4 ? CH : 1, true><<<(unsigned)((a.rows + 3) / 4), 128, 0, s>>>(a);
   } else {
     k_block_norm<FP32, CH, false><<<(unsigned)a.rows, 32 * warps, 0, s>>>(a);
   }
@@ -939,9 +939,16 @@ cudaError_t norm_launch(const NormArgs& a, int warps, cudaStream_t s) {
 
 template <bool FP32>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
-  // Up to 1024 values a lane's four chunks hold a row; wider rows take more warps.
+  // Chunks of eight values per thread.  Few rows (fewer than SMs) are a matter of
+  // latency: as many threads as the row gives work (1 x 7168 with codes 4.6 us
+  // against 5.9 at four chunks, 1 x 1024 3.4 against 5.3).  Many rows are one of
+  // bytes in flight: four chunks where the row is wide (66601 x 7168 at two: 973
+  // us against 783), two below 2048 (66601 x 1024 108 us against 115).
+  if (a.M <= 148) {
+    return a.D <= 4096 ? norm_launch<FP32, 1>(a, (a.D + 255) / 256, s) : norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
+  }
   if (a.D <= 256) return norm_launch<FP32, 1>(a, 1, s);
-  if (a.D <= 512) return norm_launch<FP32, 2>(a, 1, s);
+  if (a.D <= 2048) return norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);
 }
 
