@@ -36,6 +36,7 @@ constexpr int kDownRows = 16;  // ranks per cluster
 constexpr int kUpRows = 128;     // outputs per cluster: the MMA's M
 constexpr int kUpThreads = 192;  // loads, MMAs, four epilogue warps
 constexpr int kUpStagesMax = 8;
+constexpr uint32_t kUpClusterMax = 8;
 constexpr uint32_t kUpWBytes = kUpRows * 128;
 constexpr uint32_t kSfBytes = 1024;  // scales of 128 rows x 256 K
 
@@ -76,23 +77,29 @@ struct DownArgs {
   int M, K, R;
 };
 
-// NG groups of eight tokens.  Eight warps per CTA split K 64 ways, so that up to
-// K = 8192 a warp issues all its loads in one batch; from 65 tokens on four
-// (their sums still fit 48 KB).
+// NG groups of eight tokens, up to 64 (the tokens past 64 are a second row of
+// clusters: 70 x 7168, rank 576, 35.7 us against 37.3 with sixteen groups).  The
+// eight warps of eight CTAs split K 64 ways, so that a warp has few batches of
+// loads to wait for.
 template <int NG>
 struct DownCfg {
-  static constexpr int kWarps = NG <= 8 ? 8 : 4;
+  static constexpr int kWarps = 8;
   static constexpr int kBatch = NG <= 2 ? 4 : 2;  // steps whose loads are in flight together
 };
 
-// h[m, r0 .. r0 + 15]: cluster blockIdx.x / 8; its warps take every 64th (32nd)
-// step of 32 K.
+// h[m, r0 .. r0 + 15]: cluster blockIdx.x / 8; its warps take every 64th step of
+// 32 K.
 template <int NG>
 __global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(DownCfg<NG>::kWarps * 32, 2)
-    k_few_down(const DownArgs a) {
+    k_few_down(DownArgs a) {
   constexpr int W = DownCfg<NG>::kWarps, U = DownCfg<NG>::kBatch;
   __shared__ float sums[W][NG * 8][kDownRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Tokens from 64 blockIdx.y on.
+  a.x += (int64_t)blockIdx.y * 64 * a.K;
+  a.h += (int64_t)blockIdx.y * 64 * a.R;
+  a.M -= (int)blockIdx.y * 64;
+  if (a.M > NG * 8) a.M = NG * 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_ctarank();
@@ -356,17 +363,23 @@ __global__ void __launch_bounds__(kUpThreads)
     tc_fence_before();
   }
   cluster_barrier();
-  // Token m goes to CTA m mod S: four outputs per lane, summed in rank order.
+  // Token m goes to CTA m mod S: four outputs per lane, summed in rank order (all
+  // the peers' values on their way before the first is used).
   for (int m = (int)rank + (int)S * warp; m < a.M; m += (int)S * (kUpThreads / 32)) {
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
     const uint32_t at = smem + (uint32_t)(m * kUpRows + 4 * lane) * 4;
-    for (uint32_t c = 0; c < S; ++c) {
-      uint32_t p[4];
-      ld_shared_cluster_v4(mapa_shared(at, c), p[0], p[1], p[2], p[3]);
-      t.x += __uint_as_float(p[0]);
-      t.y += __uint_as_float(p[1]);
-      t.z += __uint_as_float(p[2]);
-      t.w += __uint_as_float(p[3]);
+    uint32_t p[kUpClusterMax][4];
+#pragma unroll
+    for (uint32_t c = 0; c < kUpClusterMax; ++c) {
+      p[c][0] = p[c][1] = p[c][2] = p[c][3] = 0;
+      if (c < S) ld_shared_cluster_v4(mapa_shared(at, c), p[c][0], p[c][1], p[c][2], p[c][3]);
+    }
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (uint32_t c = 0; c < kUpClusterMax; ++c) {
+      t.x += __uint_as_float(p[c][0]);
+      t.y += __uint_as_float(p[c][1]);
+      t.z += __uint_as_float(p[c][2]);
+      t.w += __uint_as_float(p[c][3]);
     }
     const int n = tile * kUpRows + 4 * lane;
     if (n < a.N) *reinterpret_cast<uint2*>(a.y + (int64_t)m * a.N + n) = make_uint2(round2(t.x, t.y), round2(t.z, t.w));
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(kUpThreads)
 // three stages each.
 int up_split(int tiles, int steps, int sm_count) {
   int s = 1;
-  while (s < 8 && tiles * s * 2 <= 2 * sm_count && steps >= 3 * 2 * s) s *= 2;
+  while (s < (int)kUpClusterMax && tiles * s * 2 <= 2 * sm_count && steps >= 3 * 2 * s) s *= 2;
   return s;
 }
 
@@ -439,7 +452,7 @@ cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h,
 template <int NG>
 cudaError_t down_launch(const LinearLaunch& p, const float* A_cat, float* h, cudaStream_t s) {
   const DownArgs d{reinterpret_cast<const uint16_t*>(p.x), A_cat, h, (int)p.M, p.K, p.R};
-  k_few_down<NG><<<p.R / kDownRows * kDownCluster, DownCfg<NG>::kWarps * 32, 0, s>>>(d);
+  k_few_down<NG><<<dim3(p.R / kDownRows * kDownCluster, (p.M + 63) / 64), DownCfg<NG>::kWarps * 32, 0, s>>>(d);
   return cudaGetLastError();
 }
 
@@ -463,8 +476,7 @@ cudaError_t launch_lora_linear_few(const LinearLaunch& p, const float* A_cat, co
     if (p.M <= 8) e = down_launch<1>(p, A_cat, h, s);
     else if (p.M <= 16) e = down_launch<2>(p, A_cat, h, s);
     else if (p.M <= 32) e = down_launch<4>(p, A_cat, h, s);
-    else if (p.M <= 64) e = down_launch<8>(p, A_cat, h, s);
-    else e = down_launch<16>(p, A_cat, h, s);
+    else e = down_launch<8>(p, A_cat, h, s);
     if (e != cudaSuccess) return e;
     *kernels = 1;
   }
