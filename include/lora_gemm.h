@@ -398,7 +398,7 @@ lg_status lg_lora_linear_mxfp4(const void* x, const void* x_codes, const void* x
  * is stored, and N_pre reads the stored value, so that a backward pass that
  * keeps only h' sees what this call saw.  n is rounded to bf16; its codes are
  * those of the rounded n, bit for bit what lg_mxfp4_quantize(n) or
- * lg_mx_quantize(n) writes.
+ * lg_mx_quantize(n) writes.  A row's outputs do not depend on the other rows.
  *
  * A learned norm weight w is a gate or a (scale = w - 1) of one segment.
  *

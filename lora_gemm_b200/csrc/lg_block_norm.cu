@@ -939,14 +939,10 @@ cudaError_t norm_launch(const NormArgs& a, int warps, cudaStream_t s) {
 
 template <bool FP32>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
-  // Chunks of eight values per thread.  Few rows (fewer than SMs) are a matter of
-  // latency: as many threads as the row gives work (1 x 7168 with codes 4.6 us
-  // against 5.9 at four chunks, 1 x 1024 3.4 against 5.3).  Many rows are one of
-  // bytes in flight: four chunks where the row is wide (66601 x 7168 at two: 973
-  // us against 783), two below 2048 (66601 x 1024 108 us against 115).
-  if (a.M <= 148) {
-    return a.D <= 4096 ? norm_launch<FP32, 1>(a, (a.D + 255) / 256, s) : norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
-  }
+  // Chunks of eight values per thread: four where the row is wide (66601 x 7168 at
+  // two: 973 us against 783), two up to 2048 (66601 x 1024 108 us against 115).  By
+  // the width alone, so that a row's bits do not depend on how many rows come with
+  // it; one chunk per thread would save a single row of 7168 1.2 of 5.9 us.
   if (a.D <= 256) return norm_launch<FP32, 1>(a, 1, s);
   if (a.D <= 2048) return norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);

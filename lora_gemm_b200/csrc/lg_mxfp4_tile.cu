@@ -216,22 +216,22 @@ __device__ void multiply(const Args& a, Control* ctl, uint32_t smem, uint32_t tm
       const int groups = min(2, a.q_groups - 2 * kb);
       const uint32_t sf0 = tmem + C::SF_COL + C::SF_STAGE_COLS * sf_buf;
       if (elect_lane()) {
-      for (int g = 0; g < groups; ++g) {
-        const uint32_t src = sa + A_BYTES + C::B_BYTES + (uint32_t)g * SF_GROUP;
-        const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
+        for (int g = 0; g < groups; ++g) {
+          const uint32_t src = sa + A_BYTES + C::B_BYTES + (uint32_t)g * SF_GROUP;
 #pragma unroll
-        for (int w = 0; w < 1 + C::W_GROUPS; ++w) tmem_cp_32x128b_x4_pair(sf + 4 * w, plain_rows16_desc(src + 2 * w * SF_GROUP));
-      }
-      for (int g = 0; g < groups; ++g) {
-        const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // K = 64 each, bytes 2 k and 2 k + 1 of the scale words
-          umma_mxf4_pair(d, da + 2 * (2 * g + k), db + 2 * (2 * g + k),
-                         idesc_mxf4(2 * BM, TN, 2u * (uint32_t)k, 2u * (uint32_t)k), sf, sf + 4 + sb_shift,
-                         (kb | g | k) != 0);
+          for (int w = 0; w < 1 + C::W_GROUPS; ++w)
+            tmem_cp_32x128b_x4_pair(sf0 + (uint32_t)g * C::SF_K + 4 * w, plain_rows16_desc(src + 2 * w * SF_GROUP));
         }
-      }
-      umma_commit_pair_mc(empty0 + 8 * stage, 3);
+        for (int g = 0; g < groups; ++g) {
+          const uint32_t sf = sf0 + (uint32_t)g * C::SF_K;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // K = 64 each, bytes 2 k and 2 k + 1 of the scale words
+            umma_mxf4_pair(d, da + 2 * (2 * g + k), db + 2 * (2 * g + k),
+                           idesc_mxf4(2 * BM, TN, 2u * (uint32_t)k, 2u * (uint32_t)k), sf, sf + 4 + sb_shift,
+                           (kb | g | k) != 0);
+          }
+        }
+        umma_commit_pair_mc(empty0 + 8 * stage, 3);
       }
       __syncwarp();
       if (++sf_buf == C::SF_BUFS) sf_buf = 0;
