@@ -150,6 +150,14 @@ __device__ __forceinline__ void st_stream8(float* p, bool wide, uint4 a, uint4 b
   }
 }
 
+// 1 / sqrt(x) for x > 0: the hardware's estimate (2 ulp) and one Newton step,
+// which leaves the rounding of its own last operation.  An infinite x gives 0.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  const float e = fmaf(-(x * r), r, 1.0f);
+  return r > 0.f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Raw bits of eight stream values: 16 bytes (bf16) or 32 (FP32).
 template <bool FP32>
 struct Raw8 {
@@ -298,7 +306,7 @@ __device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[
     for (int i = 0; i < 8; ++i) q[0] = fmaf(v[c][i], v[c][i], q[0]);
   }
   row_sums<1>(q, warps, slot + 1);
-  const float r = rsqrtf(q[0] / (float)D + eps);
+  const float r = inverse_root(q[0] / (float)D + eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
@@ -726,7 +734,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
         q[2] = r[1];
       }
       if (a.dn) {
-        rx = rsqrtf(q[1] * inv_d + a.eps);
+        rx = inverse_root(q[1] * inv_d + a.eps);
         k = rx * rx * rx * (q[2] * inv_d);
       }
     } else {
@@ -780,11 +788,11 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       fold(p, q);
       ok = row_group_sums<SPLIT>(q, warps, rank, slot[PASSES - 1], parity, a.wait_limit_ns, abort_flag) && ok;
       if (a.dn) {
-        rx = rsqrtf(q[0] * inv_d + a.eps);
+        rx = inverse_root(q[0] * inv_d + a.eps);
         k = rx * rx * rx * (q[2] * inv_d);
       }
       if (a.post != kNone) {
-        ru = rsqrtf(q[1] * inv_d + a.eps);
+        ru = inverse_root(q[1] * inv_d + a.eps);
         float swu = q[3] + rx * q[4] - k * q[5];
         if constexpr (PRE_L) swu -= rx * mg * q[6];
         mwu = ru * swu * inv_d;
@@ -830,7 +838,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       float q[3];
       fold(p, q);
       ok = row_group_sums<SPLIT>(q, warps, rank, slot[1], parity, a.wait_limit_ns, abort_flag) && ok;
-      ru = rsqrtf(q[0] * inv_d + a.eps);
+      ru = inverse_root(q[0] * inv_d + a.eps);
       mwu = ru * q[1] * inv_d;
       mw = q[2] * inv_d;
     }
