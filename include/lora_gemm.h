@@ -29,6 +29,15 @@
  *                   (wujieai.com) on HyperFlow's shift-12 table (host only);
  *   lg_lora_linear_noalloc   lg_lora_linear without a caller workspace.
  *
+ * and, beyond the pages, the layer's 4-bit form and what lies between two of
+ * its blocks:
+ *
+ *   lg_mxfp4_quantize, lg_mxfp4_dequantize, lg_lora_linear_mxfp4   MXFP4 codes
+ *                   and the linear layer with its base term as MXFP4 products;
+ *   lg_block_norm, lg_block_norm_backward   the norms after and before a block
+ *                   with its gate, scaled residual and modulation, and their
+ *                   gradients.
+ *
  * The pages name no random number generator.  This library draws eps from a
  * Philox4x32-10 stream (Salmon et al., "Parallel Random Numbers: As Easy as
  * 1, 2, 3", SC'11) with key = (seed mod 2^32, seed >> 32) and counter
@@ -38,7 +47,7 @@
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers on the current CUDA device,
  *     owned by the caller.  The library allocates no device memory; the
- *     scratch that lg_lora_linear needs is the caller's workspace.
+ *     scratch that an entry point needs is the caller's workspace.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Calls are asynchronous on that stream.  The return value
  *     reports argument validation and launch errors only; a device-side
