@@ -461,16 +461,20 @@ cudaError_t tile_launch(const Product& p, int pairs, uint64_t wait_limit_ns, cud
   return cudaLaunchKernelEx(&cfg, k_mxfp4_tile<TN>, tm_aq, tm_bq, tm_sa, tm_sb, tm_a, tm_b, tm_y, a);
 }
 
-// Column tile of a product: the fewest rounds of tiles over the SM pairs times
-// a tile's time, which is its columns plus what does not shrink with them (the
-// 256 token rows' share of the operand traffic, the tile's start and end).
+// Column tile of a product: the fewest rounds of tiles over the SM pairs times a
+// tile's time, which is its columns plus what does not shrink with them (the 256
+// token rows' share of the operand traffic, the tile's start and end).  h's
+// product runs beside the 4-bit part of the main one and need not fill the device:
+// the least work by its columns alone (2304 x 7168 -> 7168, rank 576, the whole
+// layer: h in 192 columns 95 us, in 128 103, in 64 118; splitting its K over idle
+// pairs instead: 105 and up).
 int tile_columns(const Product& p, int pairs) {
-  const int64_t panels = (p.M + 2 * BM - 1) / (2 * BM);
+  const int64_t panels = p.q_k > 0 ? (p.M + 2 * BM - 1) / (2 * BM) : 1;
   int best = 64;
   double least = 1e300;
   for (int tn : {256, 192, 128, 64}) {
     const int64_t tiles = panels * ((p.N + tn - 1) / tn);
-    const double cost = (double)((tiles + pairs - 1) / pairs) * (tn + 64);
+    const double cost = (double)(p.q_k > 0 ? (tiles + pairs - 1) / pairs : tiles) * (tn + 64);
     if (cost < least) {
       least = cost;
       best = tn;

@@ -59,7 +59,7 @@ def test_base_term_elementwise(M, K, N):
 
 
 @pytest.mark.parametrize("M,K,N,R", [(1, 128, 64, 64), (3, 256, 32, 576), (16, 1024, 1024, 192), (48, 384, 320, 576),
-                                     (100, 1152, 512, 192), (128, 7168, 96, 64), (130, 7168, 256, 576), (517, 384, 320, 576), (1000, 1024, 896, 64),
+                                     (100, 1152, 512, 192), (128, 7168, 96, 64), (130, 7168, 256, 576), (300, 7168, 96, 64), (700, 3200, 160, 576), (517, 384, 320, 576), (1000, 1024, 896, 64),
                                      (2304, 1024, 1024, 576), (1, 7168, 7168, 576)])
 def test_with_adapters(M, K, N, R):
     x, W, A, B = _layer(M, K, N, R, seed=M + 3 * K + N)
@@ -67,6 +67,23 @@ def test_with_adapters(M, K, N, R):
     y = _np64(_run(x, W, A, B))
     assert rel_fro(y, ref) <= TOL
     assert np.linalg.norm(y - ref, axis=1).max() <= 2 * TOL * np.linalg.norm(ref, axis=1).max()
+
+
+@pytest.mark.parametrize("R", range(64, 577, 64))
+def test_every_rank(R):
+    """Each rank picks its own column tiles for h (one to nine of 64 ranks), in both forms."""
+    for M in (40, 200):
+        x, W, A, B = _layer(M, 384, 160, R, seed=R + M)
+        ref = o4.lora_linear_mxfp4(_np64(x), _np64(W), _np64(A), _np64(B))
+        assert rel_fro(_np64(_run(x, W, A, B)), ref) <= TOL
+
+
+@pytest.mark.parametrize("N", [32, 64, 160, 192, 224, 288, 480, 544, 2048])
+def test_widths_around_the_tiles(N):
+    """Widths that end inside tiles of 64, 128, 192 and 256 columns and inside scale groups of 128."""
+    for M in (20, 260, 1100):
+        x, W, _, _ = _layer(M, 384, N, 0, seed=N + M)
+        _check_base(_run(x, W, None, None), x, W)
 
 
 def test_many_tiles():
