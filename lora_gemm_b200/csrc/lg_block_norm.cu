@@ -9,11 +9,16 @@
 //
 // Forward: one row per group of warps, each thread holding CH chunks of eight
 // consecutive values, 64 registers so that four CTAs of a 7168-wide row share an
-// SM.  The row's data are read and written past L1, which is left to the
-// modulation vectors: 3 x 4 D bytes that every row of a segment reads again (more
-// than the row itself), and that the rows resident on an SM share there, in
-// 256-bit loads.  66601 x 7168 bf16: 627 us without codes (93 % of measured HBM),
-// 732 us with MXFP4 codes (85 %: issue slots, the quantizer's share).
+// SM.  Every product and sum of the formula rounds by itself, in its order, so that
+// a row agrees to the bit with the formula in elementary FP32 operations wherever
+// the deviations do, and with it the codes, which a last bit can flip: of 65,536
+// rows of 7168 (random streams) 20 codes differ from such an evaluation's, 72 with
+// fused multiply-adds and FP32 row sums.
+// The row's data are read and written past L1, which is left to the modulation
+// vectors: 3 x 4 D bytes that every row of a segment reads again (more than the
+// row itself), and that the rows resident on an SM share there, in 256-bit loads.
+// 66601 x 7168 bf16: 640 us without codes (91 % of measured HBM), 750 us with
+// MXFP4 codes (83 %: issue slots, the quantizer's share).
 //
 // Backward: with x^ a normalised row, r its reciprocal deviation and g the
 // gradient there, the input's gradient is
@@ -150,14 +155,6 @@ __device__ __forceinline__ void st_stream8(float* p, bool wide, uint4 a, uint4 b
   }
 }
 
-// 1 / sqrt(x) for x > 0: the hardware's estimate (2 ulp) and one Newton step,
-// which leaves the rounding of its own last operation.  An infinite x gives 0.
-__device__ __forceinline__ float inverse_root(float x) {
-  const float r = rsqrtf(x);
-  const float e = fmaf(-(x * r), r, 1.0f);
-  return r > 0.f ? fmaf(0.5f * r, e, r) : r;
-}
-
 // Raw bits of eight stream values: 16 bytes (bf16) or 32 (FP32).
 template <bool FP32>
 struct Raw8 {
@@ -237,29 +234,29 @@ __device__ __forceinline__ void load_mod8(const float* base, int64_t at, bool wi
   }
 }
 
-// Sums of N values over the `warps` warps of a row (one warp: shuffles alone).
-// Each call of a row has shared memory of its own (`slot`): no barrier is
-// needed before the next call.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], int warps, float (*slot)[kMaxWarps]) {
+// Sum over each `n` lanes that differ in the low bits, n a power of two.
+template <typename T>
+__device__ __forceinline__ T lane_sum(T v, int n) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o < n) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
-  if (warps == 1) return;
+  return v;
+}
+
+// Sum over the `warps` warps of a row.  The roundings of its last additions are
+// not averaged over others and move the whole row, so those are FP64's (they
+// cost 14 us of 750 at 66601 x 7168).  Each call of a row has shared memory of
+// its own (`slot`): no barrier is needed before the next call.
+__device__ __forceinline__ double row_sum(float v, int warps, float* slot) {
+  if (warps == 1) return lane_sum((double)v, 32);
+  v = lane_sum(v, 32);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) slot[i][warp] = v[i];
-  }
+  if (lane == 0) slot[warp] = v;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = lane < warps ? slot[i][lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  }
+  const int n = 2 << (31 - __clz(warps - 1));  // `warps`, up to a power of two
+  const int w = lane & (n - 1);
+  return lane_sum(w < warps ? (double)slot[w] : 0.0, n);
 }
 
 struct NormArgs {
@@ -282,31 +279,33 @@ struct NormArgs {
 
 // Normalises the row's values in place; `live` masks chunks past D.
 template <int CH>
-__device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[CH], int kind, float eps, int D,
+__device__ __forceinline__ void normalise(float (&v)[CH][8], const bool (&live)[CH], int kind, float eps, float d,
                                           int warps, float (*slot)[kMaxWarps]) {
   if (kind == kLayer) {
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      float p = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += v[c][i];  // chunks past D hold zeros
+      for (int i = 0; i < 8; ++i) p += v[c][i];  // chunks past D hold zeros
+      s += p;
     }
-    row_sums<1>(s, warps, slot);
-    const float mean = s[0] / (float)D;
+    const float mean = (float)row_sum(s, warps, slot[0]) / d;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = live[c] ? v[c][i] - mean : 0.f;
     }
   }
-  float q[1] = {0.f};
+  float q = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
+    float p = 0.f;  // short chains: their roundings are what moves r
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[0] = fmaf(v[c][i], v[c][i], q[0]);
+    for (int i = 0; i < 8; ++i) p = fmaf(v[c][i], v[c][i], p);
+    q += p;
   }
-  row_sums<1>(q, warps, slot + 1);
-  const float r = inverse_root(q[0] / (float)D + eps);
+  const float r = rsqrtf((float)row_sum(q, warps, slot[1]) / d + eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP3
       if (live[c]) q = ld_stream(reinterpret_cast<const uint16_t*>(a.b) + at + 256 * c);
       unpack8(q, v[c]);
     }
-    if (a.post != kNone) normalise<CH>(v, live, a.post, a.eps, a.D, warps, slots);
+    if (a.post != kNone) normalise<CH>(v, live, a.post, a.eps, (float)a.D, warps, slots);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (!live[c]) continue;
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP3
       load_mod8(a.gate, mod + 256 * c, a.wide_mods, 1.0f, g);
       raw[c].get(h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(g[i], v[c][i], a.alpha * h[i]);
+      for (int i = 0; i < 8; ++i) v[c][i] = __fadd_rn(__fmul_rn(g[i], v[c][i]), __fmul_rn(a.alpha, h[i]));
       store_stream8<FP32>(a.h_out, at + 256 * c, a.wide_stream, v[c]);
     }
   } else {
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP3
     for (int c = 0; c < CH; ++c) raw[c].get(v[c]);
   }
   if (a.pre == kNone) return;
-  normalise<CH>(v, live, a.pre, a.eps, a.D, warps, slots + 2);
+  normalise<CH>(v, live, a.pre, a.eps, (float)a.D, warps, slots + 2);
   // Chunk c's K group is 2 c after chunk 0's: 1024 bytes on.
   uint8_t* sf = a.scales + mx_scale_offset(row, col / 128 * 4, a.D / 128);
 #pragma unroll
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP3
       load_mod8(a.scale, mod + 256 * c, a.wide_mods, 0.0f, s);
       load_mod8(a.shift, mod + 256 * c, a.wide_mods, 0.0f, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], 1.0f + s[i], f[i]);
+      for (int i = 0; i < 8; ++i) v[c][i] = __fadd_rn(__fmul_rn(v[c][i], 1.0f + s[i]), f[i]);
       q = pack8(v[c]);
       if (a.n) st_stream(reinterpret_cast<uint16_t*>(a.n) + at + 256 * c, q);
     }
@@ -734,7 +733,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
         q[2] = r[1];
       }
       if (a.dn) {
-        rx = inverse_root(q[1] * inv_d + a.eps);
+        rx = rsqrtf(q[1] * inv_d + a.eps);
         k = rx * rx * rx * (q[2] * inv_d);
       }
     } else {
@@ -788,11 +787,11 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       fold(p, q);
       ok = row_group_sums<SPLIT>(q, warps, rank, slot[PASSES - 1], parity, a.wait_limit_ns, abort_flag) && ok;
       if (a.dn) {
-        rx = inverse_root(q[0] * inv_d + a.eps);
+        rx = rsqrtf(q[0] * inv_d + a.eps);
         k = rx * rx * rx * (q[2] * inv_d);
       }
       if (a.post != kNone) {
-        ru = inverse_root(q[1] * inv_d + a.eps);
+        ru = rsqrtf(q[1] * inv_d + a.eps);
         float swu = q[3] + rx * q[4] - k * q[5];
         if constexpr (PRE_L) swu -= rx * mg * q[6];
         mwu = ru * swu * inv_d;
@@ -838,7 +837,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       float q[3];
       fold(p, q);
       ok = row_group_sums<SPLIT>(q, warps, rank, slot[1], parity, a.wait_limit_ns, abort_flag) && ok;
-      ru = inverse_root(q[0] * inv_d + a.eps);
+      ru = rsqrtf(q[0] * inv_d + a.eps);
       mwu = ru * q[1] * inv_d;
       mw = q[2] * inv_d;
     }
