@@ -949,7 +949,7 @@ cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
   // Chunks of eight values per thread: four where the row is wide (66601 x 7168 at
   // two: 973 us against 783), two up to 2048 (66601 x 1024 108 us against 115).  By
   // the width alone, so that a row's bits do not depend on how many rows come with
-  // it; one chunk per thread would save a single row of 7168 1.2 of 5.9 us.
+  // it; one chunk per thread would save a single row of 7168 1.2 of 6.0 us.
   if (a.D <= 256) return norm_launch<FP32, 1>(a, 1, s);
   if (a.D <= 2048) return norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);
