@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       mwu = ru * q[1] * inv_d;
       mw = q[2] * inv_d;
     }
-    // A wait that ran out is recorded; every CTA of the cluster ends the same way.
+    // A wait that ran out is recorded; the warp sends no more, so its peers' waits run out too.
     if (SPLIT > 1 && !__all_sync(0xffffffffu, ok)) break;
     const F2 ru2 = f2(ru, ru), nmw2 = f2(-ru * mw, -ru * mw), nmwu2 = f2(-ru * mwu, -ru * mwu);
     if (live) {
@@ -870,8 +870,19 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
     }
   }
   cp_async_wait(0);
-  // No CTA leaves while a peer may still send it sums.
-  if constexpr (SPLIT > 1) cluster_barrier();
+  if constexpr (SPLIT > 1) {
+    // No CTA leaves while a peer may still send it sums.  A CTA whose waits all
+    // came to an end has everything that was sent to it.  One that gave up does not
+    // know, and the barrier, after which nobody sends, does not wait for what is on
+    // its way: one thread keeps the CTA's shared memory for the microseconds that
+    // takes, and more.
+    cluster_barrier();
+    if (t == 0 && *abort_flag) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
+      }
+    }
+  }
   if (!live) return;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
