@@ -559,12 +559,14 @@ __device__ __forceinline__ void fold(const F2 (&p)[N], float (&q)[N]) {
 //
 // Without a layer norm all row sums come from one pass.  With x, b the rows, g =
 // dn (1 + scale), t = gate:
-//   rx^2 = D / sum x^2, ru^2 = D / sum b^2 (+ eps),   k = rx^3 mean(g x)
-//   dh' = dh_out + rx (g - mean g) - k x,   w = t dh',  u = ru b
-//   sum w u = ru (sum t b dh_out + rx (sum t b g - mean g sum t b) - k sum t b x)
+//   rx^2 = D / sum x^2, ru^2 = D / sum b^2 (+ eps),   k = rx^2 mean(g x)
+//   dh' = dh_out + rx (g - mean g) - k x^,   x^ = rx x,   w = t dh',  u = ru b
+//   sum w u = ru (sum t b dh_out + rx (sum t b g - mean g sum t b) - k rx sum t b x)
 //   db = ru (w - mean w - u mean(w u))
 // so the second norm's sums need no second pass over the first one's result
-// (mean g and mean w belong to layer norms).  A layer norm's row is centred
+// (mean g and mean w belong to layer norms).  k is taken as rx (rx mean(g x)), no
+// power of rx by itself: a row's rx may be 1e15 or 1e-15, and its cube is no FP32
+// number then, while k has the size of the gradient itself.  A layer norm's row is centred
 // first, so that its squares are those of centred values (a mean far above the
 // deviation would cancel in FP32): its mean takes a pass.  After a layer norm on
 // the block's output the second norm's sums are taken from dh' itself, in a pass
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       }
       if (a.dn) {
         rx = rsqrtf(q[1] * inv_d + a.eps);
-        k = rx * rx * rx * (q[2] * inv_d);
+        k = rx * (rx * (q[2] * inv_d));
       }
     } else {
       if constexpr (PRE_L) {
@@ -788,11 +790,11 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
       ok = row_group_sums<SPLIT>(q, warps, rank, slot[PASSES - 1], parity, a.wait_limit_ns, abort_flag) && ok;
       if (a.dn) {
         rx = rsqrtf(q[0] * inv_d + a.eps);
-        k = rx * rx * rx * (q[2] * inv_d);
+        k = rx * (rx * (q[2] * inv_d));
       }
       if (a.post != kNone) {
         ru = rsqrtf(q[1] * inv_d + a.eps);
-        float swu = q[3] + rx * q[4] - k * q[5];
+        float swu = q[3] + rx * q[4] - k * (rx * q[5]);
         if constexpr (PRE_L) swu -= rx * mg * q[6];
         mwu = ru * swu * inv_d;
       }
@@ -807,9 +809,9 @@ __global__ void __launch_bounds__(Back<FP32, SPLIT>::kThreads, Back<FP32, SPLIT>
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (PRE_L) x[i] = x[i] + nmx2;
-        const F2 rg = rx2 * g[i];
-        acc[1][i] = fma(rg, x[i], acc[1][i]);
-        d[i] = fma(rg, sc[i], rg + d[i]);
+        x[i] = x[i] * rx2;
+        acc[1][i] = fma(g[i], x[i], acc[1][i]);
+        d[i] = fma(rx2, fma(g[i], sc[i], g[i]), d[i]);
         if constexpr (PRE_L) d[i] = d[i] + nmg2;
         d[i] = fma(nk2, x[i], d[i]);
       }

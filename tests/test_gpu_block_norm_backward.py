@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import lora_gemm_b200 as lg
-from tests.test_gpu_block_norm import _inputs
+from tests.test_gpu_block_norm import _check_backward, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,21 @@ def test_a_row_s_meeting_is_bounded(D, stream):
     got = lg.block_norm_backward(*args)
     assert lg.get_last_device_error() == lg.LG_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("post", ["rms", "layer"])
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+@pytest.mark.parametrize("size,eps", [(2.0 ** 50, 1e-6), (2.0 ** -50, 2.0 ** -110), (0.0, 1e-30)])
+def test_rows_far_from_one(size, eps, pre, post, stream):
+    """Reciprocal deviations of 2^-50, 2^50 and, rows of zeros, 1e15: their cubes are no FP32 numbers, the
+    gradients are.  On one CTA and on a cluster, with the projection alone (no dh_out) and with a dh_out of
+    its size."""
+    for D in (1024, 4096):
+        t = _inputs(5, D, 2, stream, seed=D)
+        t["h"] *= size
+        t["b"] *= size
+        _check_backward(t, 5, D, 3, post, pre, 1.0, eps, dh_out=False)
+        t["dh"] *= size ** -1 if size else eps ** -0.5
+        got = _check_backward(t, 5, D, 3, post, pre, 1.0, eps)
+        assert all(torch.isfinite(g).all() for g in got)
