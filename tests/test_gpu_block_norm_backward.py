@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import lora_gemm_b200 as lg
-from tests.test_gpu_block_norm import _check_backward, _inputs
+from tests.test_gpu_block_norm import DEV, _check_backward, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,19 @@ def test_rows_far_from_one(size, eps, pre, post, stream):
         t["dh"] *= size ** -1 if size else eps ** -0.5
         got = _check_backward(t, 5, D, 3, post, pre, 1.0, eps)
         assert all(torch.isfinite(g).all() for g in got)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_without_norms_the_gradients_do_not_read_b(value):
+    """h' = h + gate b: db = gate dh_out and dh = dh_out whatever b holds; dgate meets b in its own column alone."""
+    t = _inputs(6, 512, 2, torch.float32, seed=11)
+    b = t["b"].clone()
+    b[4, 77] = value
+    args = dict(post=None, pre=None, segment_tokens=3)
+    dh, db, dgate, _, _ = lg.block_norm_backward(None, t["dh"], t["h"], b, t["gate"], **args)
+    want = lg.block_norm_backward(None, t["dh"], t["h"], t["b"], t["gate"], **args)
+    assert torch.equal(dh, want[0]) and torch.equal(db, want[1])
+    assert torch.equal(db, (t["gate"].repeat_interleave(3, 0) * t["dh"]).to(torch.bfloat16))
+    keep = torch.ones(2, 512, dtype=torch.bool, device=DEV)
+    keep[1, 77] = False
+    assert torch.equal(dgate[keep], want[2][keep]) and not torch.isfinite(dgate[1, 77])
