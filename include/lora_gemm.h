@@ -371,9 +371,10 @@ lg_status lg_mxfp4_dequantize(const void* codes, const void* scales, int64_t row
  *
  * The LoRA term comes from the bf16 x (which may be null when R == 0), with
  * FP32 accumulation throughout: as in lg_lora_linear_mxfp8 from bf16 roundings
- * of A_cat, of h = x A_cat^T and of B_cat for M > 128; up to 128 tokens h stays
- * FP32 and the tensor cores read h and B_cat as TF32 (ten fraction bits), so
- * the last bits of a token's outputs depend on which side of 128 its batch is.
+ * of A_cat, of h = x A_cat^T and of B_cat for M > 128; up to 128 tokens from a
+ * bf16 rounding of A_cat and TF32 roundings (ten fraction bits) of h and B_cat,
+ * so the last bits of a token's outputs depend on which side of 128 its batch
+ * is.  All of them round to nearest.
  *
  *   x_codes [M, K / 2], x_scales   lg_mxfp4_quantize(x) (or the codes that
  *                                  lg_block_norm wrote beside x).

@@ -14,10 +14,11 @@
 //   k_few_up    y = deq(x) deq(W)^T + h B_cat^T: 128 outputs per cluster of S
 //               CTAs that split K and the ranks; tcgen05 with the weights as the
 //               128-row operand and the tokens as its N (16 to 128): MXFP4
-//               stages of 256 K, then TF32 stages of 32 ranks that take B_cat
-//               and h as they are, in FP32.  All loads are TMA, 100 KB of them in
-//               flight per CTA; the CTAs' accumulators are joined in the order
-//               of their ranks through distributed shared memory.
+//               stages of 256 K, then TF32 stages of 32 ranks that take the
+//               FP32 B_cat and h, rounded by the loads.  All loads are TMA,
+//               100 KB of them in flight per CTA; the CTAs' accumulators are
+//               joined in the order of their ranks through distributed shared
+//               memory.
 //
 // k_few_up is launched as a programmatic dependent: it reads weights while
 // k_few_down still runs and waits for h only before its first load of it.
@@ -412,8 +413,8 @@ cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h,
             make_map_scales(enc, &tm_sx, p.xsf, (uint64_t)((p.M + 127) / 128) * groups, 4);
   tm_b = tm_h = tm_w;  // never read without adapters
   if (p.R > 0) {
-    ok = ok && make_map_fp32(enc, &tm_b, B_cat, (uint64_t)p.R, (uint64_t)p.N, kUpRows) &&
-         make_map_fp32(enc, &tm_h, h, (uint64_t)p.R, (uint64_t)p.M, NT);
+    ok = ok && make_map_tf32(enc, &tm_b, B_cat, (uint64_t)p.R, (uint64_t)p.N, kUpRows) &&
+         make_map_tf32(enc, &tm_h, h, (uint64_t)p.R, (uint64_t)p.M, NT);
   }
   if (!ok) {
     *driver_failed = true;

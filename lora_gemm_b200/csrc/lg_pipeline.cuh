@@ -149,14 +149,16 @@ inline bool make_map_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m
 }
 
 // Row-major FP32 matrix [outer, inner] read as tiles of box_outer rows x 32
-// columns with the 128-byte swizzle; out-of-range rows read as zero.
-inline bool make_map_fp32(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t inner,
+// columns with the 128-byte swizzle, rounded to nearest TF32 values (ten fraction
+// bits) on the way: the tensor core itself cuts the further bits off, which made a
+// sum of products 7e-4 too small.  Out-of-range rows read as zero.
+inline bool make_map_tf32(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, uint64_t inner,
                           uint64_t outer, uint32_t box_outer) {
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {inner * 4};
   cuuint32_t box[2] = {32, box_outer};
   cuuint32_t elem_strides[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_TFLOAT32, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

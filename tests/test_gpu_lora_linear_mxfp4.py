@@ -143,3 +143,21 @@ def test_wait_timeout_is_reported():
     assert status == lg.LG_ERR_DEVICE_TIMEOUT
     ref = o4.lora_linear_mxfp4(_np64(x), _np64(W), _np64(A), _np64(B))
     assert rel_fro(_np64(_run(x, W, A, B)), ref) <= TOL
+
+
+def _adapters_alone(M, K, N, R, seed):
+    """(y, the FP64 term) of a layer whose W is zero, with FP32 factors."""
+    x, _, A, B = _layer(M, K, N, R, seed)
+    y = _run(x, torch.zeros(N, K, dtype=torch.bfloat16, device=DEV), A, B)
+    return y, (_np64(x) @ _np64(A).T) @ _np64(B).T
+
+
+@pytest.mark.parametrize("M", [16, 64, 128])
+def test_few_tokens_do_not_shrink_the_adapters_term(M):
+    """The signed error of the adapters' term, as its share of the term.  Roundings to nearest have no sign:
+    the mean of y's, each below 2^-8, over M N >= 65,536 outputs has a deviation below 2^-8 / 256 = 2^-16, and
+    those of the factors and h are a thousandth of them.  2^-13 is eight deviations; factors and h cut to ten
+    fraction bits towards zero would take 2^-10.5."""
+    y, ref = _adapters_alone(M, 512, 4096, 64, seed=M)
+    bias = float(((_np64(y) - ref) * ref).sum() / (ref * ref).sum())
+    assert abs(bias) <= 2.0 ** -13, bias
