@@ -30,6 +30,7 @@
 // columns, so the column sums dgate, dscale and dshift stay in registers over
 // the CTA's rows; one partial row per CTA goes to the workspace and a second
 // kernel adds the partials of a segment in a fixed order.
+#include <atomic>
 #include <initializer_list>
 
 #include "lg_internal.h"
@@ -43,6 +44,8 @@ namespace {
 constexpr int kNone = 0, kLayer = 2;  // LG_NORM_NONE, LG_NORM_LAYER (LG_NORM_RMS needs no test)
 constexpr int kCodesMxfp4 = 2;  // LG_CODES_MXFP4; any other nonzero format is MXFP8
 constexpr int kMaxWarps = 32;  // of a row in one CTA
+
+std::atomic<bool> g_launched{false};  // a kernel that waits, so that the error word may be set
 
 // Eight consecutive values of a row as FP32; loads and stores of the stream
 // data do not allocate in L1.
@@ -1081,6 +1084,7 @@ cudaError_t back_launch(BackArgs& a, int64_t chunks, int T, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = SPLIT > 1 ? 1 : 0;
+  if (SPLIT > 1) g_launched.store(true);
   return cudaLaunchKernelEx(&cfg, k_block_norm_backward<FP32, SPLIT, PRE_L, POST_L>, (const BackArgs)a);
 }
 
@@ -1149,6 +1153,9 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardLaunch& p, int* ke
   return cudaGetLastError();
 }
 
-cudaError_t take_norm_error(int* value) { return take_device_error(value); }
+cudaError_t take_norm_error(int* value) {
+  *value = 0;
+  return g_launched.load() ? take_device_error(value) : cudaSuccess;
+}
 
 }  // namespace lg

@@ -147,7 +147,9 @@ void set_variant_override(int v);
 // Device error word of the current device: read and clear (synchronous on s).
 cudaError_t read_and_clear_device_error(cudaStream_t s, int* value);
 
-// The same for the error words of the MXFP4 and norm kernels (no synchronization before).
+// The same for the error words of the MXFP4 and norm kernels (no synchronization
+// before).  A word is a copy of 9 us: one whose kernels the process has never
+// launched is not read.
 cudaError_t take_tile_error(int* value);
 cudaError_t take_few_error(int* value);
 cudaError_t take_norm_error(int* value);

@@ -22,6 +22,8 @@
 //
 // k_few_up is launched as a programmatic dependent: it reads weights while
 // k_few_down still runs and waits for h only before its first load of it.
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "lg_internal.h"
@@ -30,6 +32,8 @@
 namespace lg {
 
 namespace {
+
+std::atomic<bool> g_launched{false};  // so that the error word may be set
 
 constexpr int kDownCluster = 8;
 constexpr int kDownRows = 16;  // ranks per cluster
@@ -447,6 +451,7 @@ cudaError_t up_launch(const LinearLaunch& p, const float* B_cat, const float* h,
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.R > 0 ? 2 : 1;  // without adapters nothing waits for the kernel before
+  g_launched.store(true);
   return cudaLaunchKernelEx(&cfg, k_few_up<NT>, tm_w, tm_x, tm_sw, tm_sx, tm_b, tm_h, a);
 }
 
@@ -459,7 +464,10 @@ cudaError_t down_launch(const LinearLaunch& p, const float* A_cat, float* h, cud
 
 }  // namespace
 
-cudaError_t take_few_error(int* value) { return take_device_error(value); }
+cudaError_t take_few_error(int* value) {
+  *value = 0;
+  return g_launched.load() ? take_device_error(value) : cudaSuccess;
+}
 
 bool few_tokens(int64_t M) { return M <= 128; }
 

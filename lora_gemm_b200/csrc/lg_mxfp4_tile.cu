@@ -32,12 +32,16 @@
 // Warp 0 loads, warp 1 owns tensor memory and issues copies and MMAs from one
 // thread, warps 2-9 are the epilogue (bf16, TMA stores).  Every mbarrier wait
 // is bounded, as in the panel kernel.
+#include <atomic>
+
 #include "lg_internal.h"
 #include "lg_pipeline.cuh"
 
 namespace lg {
 
 namespace {
+
+std::atomic<bool> g_launched{false};  // so that the error word may be set
 
 constexpr int BM = 128;  // token rows per CTA
 constexpr uint32_t A_BYTES = BM * 128;
@@ -458,6 +462,7 @@ cudaError_t tile_launch(const Product& p, int pairs, uint64_t wait_limit_ns, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.dependent ? 1 : 0;
+  g_launched.store(true);
   return cudaLaunchKernelEx(&cfg, k_mxfp4_tile<TN>, tm_aq, tm_bq, tm_sa, tm_sb, tm_a, tm_b, tm_y, a);
 }
 
@@ -496,7 +501,10 @@ cudaError_t product_launch(const Product& p, int sm_count, uint64_t wait_limit_n
 
 }  // namespace
 
-cudaError_t take_tile_error(int* value) { return take_device_error(value); }
+cudaError_t take_tile_error(int* value) {
+  *value = 0;
+  return g_launched.load() ? take_device_error(value) : cudaSuccess;
+}
 
 cudaError_t launch_lora_linear_tiles(const LinearLaunch& p, uint16_t* h, int* kernels, cudaStream_t s,
                                      bool* driver_failed) {
