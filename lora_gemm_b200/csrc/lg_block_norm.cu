@@ -960,11 +960,13 @@ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) ==
 
 template <bool FP32, int CH>
 cudaError_t norm_launch(const NormArgs& a, int warps, cudaStream_t s) {
-  if (CH < 4 && warps == 1) {
-    k_block_norm<FP32, CH < 4 ? CH : 1, true><<<(unsigned)((a.rows + 3) / 4), 128, 0, s>>>(a);
-  } else {
-    k_block_norm<FP32, CH, false><<<(unsigned)a.rows, 32 * warps, 0, s>>>(a);
-  }
+  k_block_norm<FP32, CH, false><<<(unsigned)a.rows, 32 * warps, 0, s>>>(a);
+  return cudaGetLastError();
+}
+// Rows of one warp, four to a CTA.
+template <bool FP32, int CH>
+cudaError_t narrow_launch(const NormArgs& a, cudaStream_t s) {
+  k_block_norm<FP32, CH, true><<<(unsigned)((a.rows + 3) / 4), 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -974,7 +976,8 @@ cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
   // two: 973 us against 783), two up to 2048 (66601 x 1024 108 us against 115).  By
   // the width alone, so that a row's bits do not depend on how many rows come with
   // it; one chunk per thread would save a single row of 7168 1.2 of 6.0 us.
-  if (a.D <= 256) return norm_launch<FP32, 1>(a, 1, s);
+  if (a.D <= 256) return narrow_launch<FP32, 1>(a, s);
+  if (a.D <= 512) return narrow_launch<FP32, 2>(a, s);
   if (a.D <= 2048) return norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
   return norm_launch<FP32, 4>(a, (a.D + 1023) / 1024, s);
 }
