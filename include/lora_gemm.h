@@ -404,7 +404,9 @@ lg_status lg_lora_linear_mxfp4(const void* x, const void* x_codes, const void* x
  *   N(v) = (v - mean v) / sqrt(mean((v - mean v)^2) + eps)   LG_NORM_LAYER
  *   N(v) = v                                             LG_NORM_NONE
  *
- * Statistics and sums are FP32.  h' is rounded to the stream's type when it
+ * Statistics and sums are FP32, the last additions of a row's sums FP64; a row
+ * whose sum of squares passes FP32's range (3.4e38) normalises to zeros, or to
+ * NaN where it holds infinities.  h' is rounded to the stream's type when it
  * is stored, and N_pre reads the stored value, so that a backward pass that
  * keeps only h' sees what this call saw.  n is rounded to bf16; its codes are
  * those of the rounded n, bit for bit what lg_mxfp4_quantize(n) or

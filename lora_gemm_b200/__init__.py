@@ -629,7 +629,9 @@ def block_norm(h, b=None, gate=None, scale=None, shift=None, alpha=1.0, eps=1e-6
     h [M, D] is the residual stream (bf16 or FP32), b [M, D] bf16 the block's
     output; gate, scale, shift FP32 [S, D] hold one row per segment of
     segment_tokens rows (default: one segment).  post and pre are "rms",
-    "layer" or None; b None (the norm that opens a network) needs post None.
+    "layer" or None; without b (the norm that opens a network) there is nothing
+    to norm after the block: post "rms", the default, counts as None then, and
+    "layer" is refused.
     quant "mxfp8" or "mxfp4" also quantizes n, as mx_quantize(n) or
     mxfp4_quantize(n) would.  Returns (h', n, (codes, scales)); h' is h itself
     without b, n is None without pre, the pair is None without quant.  Outputs
@@ -693,7 +695,8 @@ def block_norm_backward(dn, dh_out, h_out, b=None, gate=None, scale=None, alpha=
     pre) and of h' (the stream's type; None for zero), h_out the h' that
     block_norm returned, the rest its arguments.  Returns (dh, db, dgate,
     dscale, dshift), the last three FP32 [S, D]; db and dgate are None without
-    b, dscale and dshift without pre.  dh may be dh_out itself."""
+    b, dscale and dshift without pre.  Without b post counts as in block_norm.
+    dh may be dh_out itself."""
     if b is None and post == "rms":
         post = None
     M, D, seg, S = _norm_args(h_out, post, pre, segment_tokens)

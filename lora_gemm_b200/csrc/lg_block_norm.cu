@@ -5,15 +5,17 @@
 //
 // (RMS or layer norms over the D values of a row; gate, scale and shift per
 // segment of rows).  Both directions touch every row once and are bound by
-// HBM; the statistics are FP32 sums over the row held in registers.
+// HBM; the statistics are sums over the row held in registers, FP32 but for the
+// forward's last additions (row_sum).  Squares are FP32's: a row whose sum of
+// squares passes 3.4e38 has an infinite deviation.
 //
 // Forward: one row per group of warps, each thread holding CH chunks of eight
 // consecutive values, 64 registers so that four CTAs of a 7168-wide row share an
-// SM.  Every product and sum of the formula rounds by itself, in its order, so that
-// a row agrees to the bit with the formula in elementary FP32 operations wherever
-// the deviations do, and with it the codes, which a last bit can flip: of 65,536
-// rows of 7168 (random streams) 20 codes differ from such an evaluation's, 72 with
-// fused multiply-adds and FP32 row sums.
+// SM.  Every product and sum of the formula rounds by itself, in its order (but for the
+// squares, which are fused into their sum), so that a row agrees to the bit with the
+// formula in elementary FP32 operations wherever the deviations do, and with it the
+// codes, which a last bit can flip: of 65,536 rows of 7168 (random streams) 20 codes
+// differ from such an evaluation's, 72 with fused multiply-adds and FP32 row sums.
 // The row's data are read and written past L1, which is left to the modulation
 // vectors: 3 x 4 D bytes that every row of a segment reads again (more than the
 // row itself), and that the rows resident on an SM share there, in 256-bit loads.
@@ -412,9 +414,10 @@ __global__ void __launch_bounds__(ONE ? 128 : (CH == 4 ? 512 : 1024), ONE || FP3
 constexpr int kBackStagesMax = 4;
 // A backward CTA: at most 448 threads (of eight columns each), two per SM, so 72
 // registers a thread.  FP32 rows hold more of them (spills at 72): where one CTA
-// of up to 256 threads has the row, three per SM, 80 registers (33001 x 1024: 166
-// us against 207); a wider row on more CTAs of that size loses more to their
-// meeting (33001 x 7168 on four: 1423 us against 1050 on two).
+// of up to 256 threads has the row, three per SM, 80 registers (33001 x 1024: 156
+// us against 198); a wider row on more CTAs of that size loses more to their
+// meeting (33001 x 7168 on four: 1227 us against 946 on two; 33001 x 4096, where
+// two are 256 threads wide as well, would gain: 549 on two of these, 684 now).
 constexpr int kBackThreads = 448;
 constexpr int kBackSmem = 106 * 1024;  // modulation and row stages
 template <bool FP32, int SPLIT>
@@ -973,9 +976,9 @@ cudaError_t narrow_launch(const NormArgs& a, cudaStream_t s) {
 template <bool FP32>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
   // Chunks of eight values per thread: four where the row is wide (66601 x 7168 at
-  // two: 973 us against 783), two up to 2048 (66601 x 1024 108 us against 115).  By
-  // the width alone, so that a row's bits do not depend on how many rows come with
-  // it; one chunk per thread would save a single row of 7168 1.2 of 6.0 us.
+  // two: 850 us against 641), two up to 2048 (66601 x 1024 at four: 97 us against
+  // 95).  By the width alone, so that a row's bits do not depend on how many rows
+  // come with it; one chunk per thread would save a single row of 7168 1.2 of 6.0 us.
   if (a.D <= 256) return narrow_launch<FP32, 1>(a, s);
   if (a.D <= 512) return narrow_launch<FP32, 2>(a, s);
   if (a.D <= 2048) return norm_launch<FP32, 2>(a, (a.D + 511) / 512, s);
@@ -1007,9 +1010,13 @@ Chunks back_chunks(int64_t M, int D, int64_t seg) {
   Chunks c;
   c.segments = (M + seg - 1) / seg;
   const int64_t rest = M - (c.segments - 1) * seg;
-  // One wave: the clusters that 148 SMs hold (at most eight CTAs each).  A
+  // The clusters that the threads of 148 SMs hold (at most eight CTAs each).  A
   // chunk's partial sums cost as much traffic as about one of its rows, and its
-  // rows follow one another: not less than four of them.
+  // rows follow one another: not less than four of them.  This counts threads
+  // alone: it is one wave where a CTA has near 448 of them, and up to two where
+  // the shared memory of their rings holds fewer CTAs than that (of the planned
+  // 7, 3 and 3 per SM 5, 2 and 2 fit at bf16 widths of 1024, 4096 and 16384:
+  // 33001 x 4096 takes 457 us, 33001 x 7168 584).
   const int split = back_split<FP32>(D), threads = back_threads<FP32>(D);
   const int64_t resident = (split == 1 ? Back<FP32, 1>::kCtas * Back<FP32, 1>::kThreads : 2 * kBackThreads) / threads;
   const int64_t target = 148 * (resident > 8 ? 8 : resident) / split;

@@ -1,9 +1,11 @@
 // lg_lora_linear_mxfp4 for few tokens (M <= 128): bound by reading the weights
-// and factors once, 17/32 bytes per weight and 4 per factor.
+// and factors once, 17/32 bytes per weight and 4 per factor (past 64 tokens A_cat
+// a second time, from L2).
 //
 // The tile kernel would multiply 256 token rows, give each SM pair whole
-// columns of K, and read the factors twice (a pass copies them to bf16): 65 x
-// 7168 -> 7168 at rank 576 takes it 53 us.  Here the weights are the wide
+// columns of K, and read the factors twice (a pass copies them to bf16): 129 x
+// 7168 -> 7168 at rank 576 takes it 45 us, 128 tokens take 40 here and one token
+// 16.5 (9.5 without adapters).  Here the weights are the wide
 // operand and the tokens the narrow one, and K is split:
 //
 //   k_few_down  h = x A_cat^T: a cluster of eight CTAs per 16 ranks, K spread
@@ -20,8 +22,18 @@
 //               joined in the order of their ranks through distributed shared
 //               memory.
 //
-// k_few_up is launched as a programmatic dependent: it reads weights while
-// k_few_down still runs and waits for h only before its first load of it.
+// k_few_up is launched as a programmatic dependent and waits for k_few_down only
+// before its first load of h: it reads weights beside it on the SMs that have room.
+// At rank 192 k_few_down's 96 CTAs leave most of them free; at rank 576 it has 288,
+// whose 114 to 128 registers for each of 256 threads leave next to none, and the
+// two run one after the other.
+//
+// A_cat is rounded to bf16, h and B_cat to TF32: one product each, as in the
+// library's other layers, against an FP32 evaluation of the adapters' term a
+// difference of 0.0018 in y (relative Frobenius; y's own rounding is 0.0016, and the
+// base term's 4-bit codes move it by 0.16).  As pairs of bf16 parts, two products
+// for h and three for y, the term would be FP32's: 17.9 us instead of 16.4 for one
+// token 7168 -> 7168 at rank 576, 102 instead of 92 for 128 x 28672 -> 7168.
 #include <atomic>
 
 #include <cuda_bf16.h>

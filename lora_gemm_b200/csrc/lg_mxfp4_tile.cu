@@ -23,6 +23,12 @@
 //     thread that issues the MMAs also issues the scale copies (tcgen05.cp):
 //     tcgen05 executes one thread's copies and MMAs in order, so neither needs
 //     a wait of its own.
+//   * A_cat, h and B_cat are rounded to bf16, as in the other layers: against an
+//     FP32 evaluation of the adapters' term a difference of 0.0022 in y (relative
+//     Frobenius; y's own rounding is 0.0016, and the base term's 4-bit codes move
+//     it by 0.16).  Pairs of bf16 parts instead would take a second product for h
+//     and two more for y: 0.5 of 1.6 ms at 16384 x 28672 -> 7168, rank 576, by the
+//     rate.
 //   * tiles run over blocks of eight panels, panels fastest: the 74 tiles in
 //     flight share eight panels of x and nine tiles of W in L2.
 //   * the second launch is a programmatic dependent of the first: its 4-bit
