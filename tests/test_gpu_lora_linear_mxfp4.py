@@ -161,3 +161,30 @@ def test_few_tokens_do_not_shrink_the_adapters_term(M):
     y, ref = _adapters_alone(M, 512, 4096, 64, seed=M)
     bias = float(((_np64(y) - ref) * ref).sum() / (ref * ref).sum())
     assert abs(bias) <= 2.0 ** -13, bias
+
+
+@pytest.mark.parametrize("M", [5, 100, 300])
+def test_non_finite_factors_stay_where_they_belong(M):
+    """A NaN or an infinity in a row of B_cat makes its output column non-finite (the NaN: NaN) and leaves the other
+    columns' bits; a NaN in A_cat reaches every output; a factor of 2^100 keeps its term."""
+    x, W, A, B = _layer(M, 256, 160, 64, seed=M)
+    want = _run(x, W, A, B)
+    assert torch.isfinite(want).all()
+    B2 = B.clone()
+    B2[7, 3], B2[9, 60], B2[159, 0] = float("nan"), float("inf"), -float("inf")
+    y = _run(x, W, A, B2)
+    assert torch.isnan(y[:, 7]).all() and not torch.isfinite(y[:, [9, 159]]).any()
+    keep = [n for n in range(160) if n not in (7, 9, 159)]
+    assert torch.equal(y[:, keep], want[:, keep])
+    A2 = A.clone()
+    A2[5, 200] = float("nan")
+    assert torch.isnan(_run(x, W, A2, B)).all()
+    B3 = torch.zeros_like(B)
+    B3[1, 1] = 2.0 ** 100
+    ref = _np64(lg.lora_linear_mxfp4(None, lg.mxfp4_quantize(x), lg.mxfp4_quantize(W), None, None))
+    big = _np64(_run(x, W, A, B3))
+    h = _np64(x) @ _np64(A)[1]
+    # Two roundings of the factors' term to bf16 or nearer, y's, and A's among K products.
+    tol = 3 * 2.0 ** -8 * np.abs(h) + 2.0 ** -8 * (np.abs(_np64(x)) @ np.abs(_np64(A)[1]))
+    assert (np.abs(big[:, 1] - h * 2.0 ** 100) <= tol * 2.0 ** 100).all()
+    assert np.array_equal(np.delete(big, 1, 1), np.delete(ref, 1, 1))
